@@ -401,6 +401,130 @@ KVB_API kvb_status kvb_segment_cosine(const void* K, const void* nextK, int32_t 
                               int32_t frame_h, int32_t frame_w, int32_t seg_h, int32_t seg_w,
                               int32_t head_dim, kvb_dtype dtype, float* sim, void* stream);
 
+/* Rotary positions over three axes (time, row, column of a video token; any other
+ * three axes do).  The backbone rotates queries and keys with these before they
+ * reach a cache (DensityKV, Supplementary "Post-RoPE Attention Geometry").
+ *   Pair j (0 <= j < axis_pairs[a]) of axis a turns by
+ *     angle = pos[token][a] * base^(-j / axis_pairs[a]),
+ *     (x, y) -> (x cos - y sin, x sin + y cos);
+ *   axis 0's pairs come first, then axis 1's, then axis 2's; pairs past their sum
+ *   are copied (a head rotated in part).  inverse != 0 turns by -angle: the
+ *   transpose, which is also the gradient with respect to X of the rotation.
+ *   Rotating by the difference of two positions moves a rotated key from one to
+ *   the other (a memory key's frame index to 0, say); positions may be negative.
+ * X, out: device, rows of head_dim contiguous elements; element (h, t) starts
+ *   h * head_stride + t * token_stride elements from the pointer, so the
+ *   projection's [N][H][d] is turned head-major ([H][N][d]) in the same pass.
+ *   out may equal X with equal strides; otherwise the two must not overlap.
+ * pos: device int32 [n_tokens][3].  axis_pairs: host int32[3], each >= 0, their
+ *   sum <= head_dim / 2.  base > 0, finite.  heads 1..65535, n_tokens >= 0,
+ *   head_dim a multiple of 8 up to 256.
+ * X, out and every stride (in bytes) must be multiples of 16 (KVB_E_INVAL).
+ * Angles are formed and reduced in fp64, products and sums in fp32, one rounding
+ * to the output type. */
+typedef enum { KVB_ROPE_INTERLEAVED = 0, /* pair j = elements (2j, 2j+1) */
+               KVB_ROPE_HALVES = 1       /* pair j = elements (j, j + head_dim/2) */
+} kvb_rope_pairing;
+KVB_API kvb_status kvb_rope(const void* X, const int32_t* pos, int32_t heads, int32_t n_tokens, int32_t head_dim,
+                            kvb_dtype dtype, const int32_t* axis_pairs, float base, kvb_rope_pairing pairing,
+                            int32_t inverse, int64_t x_head_stride, int64_t x_token_stride, void* out,
+                            int64_t out_head_stride, int64_t out_token_stride, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * A K/V cache held in 8 bits with a scale for each block of tokens and head, for
+ * callers that manage their own caches: rows are appended, attended, weighed and
+ * cut to a budget in place of the bank's density or similarity policy.
+ *
+ * A cached value is code * scale: code in FP8 E4M3 (the encoding of
+ * KVB_STORE_FP8_E4M3), scale the f32 of its (head, block of `block` tokens), K and
+ * V apart.  kvb_q8_append writes power-of-two scales, the smallest with
+ * max|x| / scale <= 448 over the block, so scaling loses nothing and the only
+ * rounding is E4M3's (step 2^-3 of a value's binade, above 2^-15 of the block's
+ * largest).  The attention and weight kernels accept any positive finite scale.
+ *
+ * Sequences of a batch are further heads (heads = batch x K/V heads).  Query heads
+ * that share a K/V head are further rows of it: [batch][Hq][n][d] queries are, as
+ * they lie, [heads][Hq/Hkv * n][d].  Rows see every token their head holds, as in
+ * kvb_attend (no mask); a head that holds none gives rows of zeros with lse -inf.
+ *
+ * All arrays are the caller's device memory; K and V 16-byte aligned, the others
+ * by their type.  `len` is read on the device, so a captured call follows the
+ * cache's growth; lengths outside [0, capacity] are taken as the nearer bound.
+ * Nothing at or behind a head's length is read as a value (it may hold anything)
+ * and attention, weights and eviction leave it as it was.
+ * Calls that touch the same cache or workspace are ordered by the caller (one
+ * stream, or events); calls on different caches and workspaces may overlap.
+ * ---------------------------------------------------------------------------- */
+typedef struct {
+  int32_t heads;    /* 1..1024 */
+  int32_t head_dim; /* d: 64 or 128 */
+  int32_t capacity; /* tokens per head, a positive multiple of block, at most 2^24 */
+  int32_t block;    /* tokens per scale: 16, 32, 64 or 128 */
+  uint8_t* K;       /* [heads][capacity][d] E4M3 codes */
+  uint8_t* V;
+  float* k_scale;   /* [heads][capacity / block] */
+  float* v_scale;
+  int32_t* len;     /* [heads] tokens held */
+  float* mass;      /* [heads][capacity] accumulated attention weight, or NULL */
+  int32_t* status;  /* one word, zeroed by the caller: receives the first device-side
+                       failure (KVB_E_DEVICE_*), or NULL */
+} kvb_q8_cache;
+
+/* Bytes of device scratch (256-byte aligned) the calls below need on this cache
+ * for up to max_queries rows per head of this type; 0 if the sizes are invalid.
+ * Its contents need no initialisation and mean nothing between calls. */
+KVB_API size_t kvb_q8_workspace_size(const kvb_q8_cache* c, int32_t max_queries, kvb_dtype dtype);
+
+/* Append n tokens to every head: token i of head h is written at start[h] + i and
+ * len[h] becomes start[h] + n (start NULL: the present len).  K and V are rows of d
+ * contiguous elements of `dtype`; row (h, i) starts h * head_stride + i *
+ * token_stride elements from its pointer (pointers and strides multiples of 16
+ * bytes, else KVB_E_INVAL).  A block that already holds tokens before start[h]
+ * keeps the larger of its scale and the new tokens' one; where that grows, its
+ * older codes are rounded anew to the grown scale.  `mass`, if the cache has it, is
+ * set to 0 for the new tokens.  A head without room (start[h] < 0 or start[h] + n >
+ * capacity) is left as it was, and KVB_E_DEVICE_BOUNDS goes to the status word.
+ * Values beyond 448 * 2^119 saturate, infinities become +-448 codes and take no part
+ * in the scale, NaN stays NaN.  n >= 0; n == 0 with start NULL does nothing. */
+KVB_API kvb_status kvb_q8_append(const kvb_q8_cache* c, const void* K, int64_t k_head_stride, int64_t k_token_stride,
+                                 const void* V, int64_t v_head_stride, int64_t v_token_stride, int32_t n,
+                                 kvb_dtype dtype, const int32_t* start, void* stream);
+
+/* O = softmax(scale Q K^T) V over the tokens each head holds.  Q, O: device
+ * [heads][Nq][d] of `dtype`, 16-byte aligned; lse: device [heads][Nq] f32 (natural
+ * log of the sum of exp(scale q.k)) or NULL; scale > 0, or 0 => 1/sqrt(d).  One query
+ * (a single token) up to whole chunks.  bf16 runs on the tensor cores: Q enters as
+ * two E4M3 parts of each element or as fp16 with a power of two per row, weights as
+ * fp16, sums fp32; f32 runs on CUDA cores (small problems).  Infinite or NaN queries
+ * give NaN rows. */
+KVB_API kvb_status kvb_q8_attend(const kvb_q8_cache* c, const void* Q, int32_t Nq, kvb_dtype dtype, float scale,
+                                 void* O, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The attention weight each held token received from these queries:
+ *   mass[h][k] = decay * prev[h][k] + sum_r exp(scale q_r.k - lse[h][r])
+ * with lse as kvb_q8_attend returned it (rows of lse -inf weigh nothing).  prev:
+ * device [heads][capacity] f32, NULL (taken as 0) or the cache's own `mass`; other
+ * overlaps with it are not allowed.  c->mass is required (KVB_E_INVAL).  Sums run in
+ * a fixed order: equal inputs give equal bits. */
+KVB_API kvb_status kvb_q8_mass(const kvb_q8_cache* c, const void* Q, int32_t Nq, kvb_dtype dtype, float scale,
+                               const float* lse, float decay, const float* prev, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* Cut every head of `src` to at most `budget` tokens by their accumulated weight
+ * and write what stays, in its order, to `dst`: the first `sink` and the last
+ * `recent` tokens stay, and of the rest the budget - sink - recent with the largest
+ * mass (of equal ones, and of -0 and 0, those at lower positions; NaN counts as the least).  A
+ * head of at most budget tokens is copied.  dst->len receives min(len, budget),
+ * kept (device int32 [heads][budget], or NULL) the positions in src, and dst->mass,
+ * if not NULL, the kept tokens' mass.  A block of dst takes the largest scale among
+ * its tokens, and codes from blocks of smaller scale are rounded anew to it.
+ * src->mass is required; dst has the same heads, head_dim and block, a capacity of at
+ * least budget, and arrays of its own (none of src's; KVB_E_INVAL for equal
+ * pointers).  budget >= 1, sink, recent >= 0, sink + recent <= budget. */
+KVB_API kvb_status kvb_q8_evict(const kvb_q8_cache* src, const kvb_q8_cache* dst, int32_t budget, int32_t sink,
+                                int32_t recent, int32_t* kept, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
 #ifdef __cplusplus
 }
 #endif

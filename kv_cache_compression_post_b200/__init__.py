@@ -1,4 +1,4 @@
-"""kvb: historical KV-bank management (DensityKV, Forcing-KV) on sm_100a.
+"""kvb: historical KV-bank management (DensityKV, Forcing-KV), rotary positions and an 8-bit cache on sm_100a.
 
 The binding lives in ``kv_cache_compression_post_b200.kvb`` (loaded on first
 use: importing it fails loudly if ``libkvb.so`` has not been built with
@@ -8,7 +8,8 @@ use: importing it fails loudly if ``libkvb.so`` has not been built with
 
 
 def __getattr__(name):
-    if name.startswith("kvb_") or name in ("KvbError", "make_config", "lib", "LIB_PATH", "Bank", "PAGES_PRESET") \
+    if name.startswith("kvb_") or name in ("KvbError", "make_config", "lib", "LIB_PATH", "Bank", "PAGES_PRESET",
+                                            "Q8Cache", "rope") \
             or name.startswith("KVB_"):
         from . import kvb as _kvb
         return getattr(_kvb, name)

@@ -1,0 +1,257 @@
+// The 8-bit block-scaled K/V cache: what its kernels share (views, E4M3 conversions,
+// the split of (head, row tile, key tile) work over CTAs) and their launchers.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "kvb.h"
+#include "kvb_device.cuh"
+
+namespace kvb {
+
+constexpr int kQ8MaxHeads = 1024;
+constexpr int kQ8MaxCapacity = 1 << 24;
+constexpr int kQ8MaxCtas = 160;  // grid cap of the kernels that split work (>= the SMs of a B200)
+
+struct Q8View {
+  int H, d, cap, block;
+  const uint8_t* K;
+  const uint8_t* V;
+  const float* ks;
+  const float* vs;
+  const int* len;
+  int* status;
+};
+
+__device__ __forceinline__ int q8_len(const int* len, int h, int cap) { return min(max(len[h], 0), cap); }
+
+// two E4M3 codes (low 16 bits) -> two fp16 (exact)
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t c) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c & 0xFFFFu), __NV_E4M3);
+  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+}
+__device__ __forceinline__ float2 e4m3x2_to_f32x2(uint32_t c) {
+  const uint32_t h = e4m3x2_to_f16x2(c);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// two floats -> two E4M3 codes, to nearest even, saturating
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
+  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float2 unpack_bf16x2(uint32_t w) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+}
+// 2^e as a float, e in [-126, 127]
+__device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
+// floor(log2 |x|) of a normal float; -126 or less for zero and subnormals
+__device__ __forceinline__ int exponent_of(float x) { return static_cast<int>((__float_as_uint(x) >> 23) & 0xFFu) - 127; }
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// ------------------------------------------------------------------ work split
+// A unit is (head h, row tile r); it walks the T[h] key tiles its head holds.  The
+// key tiles of every unit, in the order of (h, r), are one sequence of costs (w per
+// tile, wlast in a head's last row tile); CTA c of G takes the tiles that start in
+// [ceil(c total / G), ceil((c+1) total / G)).  Heads of very different length, one
+// row or many, thus load every SM alike.  A unit cut between CTAs leaves one partial
+// per piece: in a CTA's slot 0 for its first piece, slot 1 for its last one.
+struct Q8Sched {
+  long long C[kQ8MaxHeads + 1];  // cost before each head
+  int T[kQ8MaxHeads];
+  long long total;
+  int G;
+};
+
+struct Q8Split {
+  const Q8Sched* s;
+  int H, nrt;      // row tiles per head
+  int w, wlast;    // cost of a key tile; in the last row tile
+  __device__ int wt(int r) const { return r == nrt - 1 ? wlast : w; }
+  __device__ long long start(int h, int r) const { return s->C[h] + static_cast<long long>(r) * w * s->T[h]; }
+  __device__ int cta_of(long long x) const { return static_cast<int>((x * s->G) / s->total); }
+  __device__ long long lo(int c) const { return (static_cast<long long>(c) * s->total + s->G - 1) / s->G; }
+};
+
+// Filled by the whole CTA (blockDim.x a multiple of 32); `min_cost`: a CTA's share is
+// at least this much.  Ends with a __syncthreads().
+__device__ __forceinline__ void q8_build_sched(Q8Sched* s, const int* len, int cap, int H, int nrt, int tile, int w,
+                                               int wlast, int grid, int min_cost) {
+  for (int h = threadIdx.x; h < H; h += blockDim.x) s->T[h] = (q8_len(len, h, cap) + tile - 1) / tile;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    const long long per = static_cast<long long>(nrt - 1) * w + wlast;
+    long long carry = 0;
+    for (int b = 0; b < H; b += 32) {
+      const long long n = b + lane < H ? per * s->T[b + lane] : 0;
+      long long x = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (b + lane < H) s->C[b + lane] = carry + x - n;
+      carry += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) {
+      s->C[H] = carry;
+      s->total = carry;
+      const long long g = carry / min_cost;
+      s->G = static_cast<int>(g < 1 ? 1 : (g < grid ? g : grid));
+    }
+  }
+  __syncthreads();
+}
+
+struct Q8Piece {
+  int h, r, j0, j1;
+  int npieces;  // pieces the unit is cut into
+  int which;    // this piece's slot
+  int cfirst;   // CTA of the unit's first piece
+  int wfirst;   // slot of it
+};
+
+__device__ __forceinline__ void q8_unit_pieces(const Q8Split& S, int h, int r, Q8Piece& pc) {
+  const long long cu = S.start(h, r);
+  const int w = S.wt(r);
+  const int cf = S.cta_of(cu), cl = S.cta_of(cu + static_cast<long long>(w) * (S.s->T[h] - 1));
+  pc.npieces = cl - cf + 1;
+  pc.cfirst = cf;
+  // the key tile before this unit, in the order of all units, starts wprev earlier
+  const int wprev = r > 0 ? S.w : S.wlast;
+  pc.wfirst = (cu == 0 || S.cta_of(cu - wprev) < cf) ? 0 : 1;
+}
+
+// The pieces of one CTA, in order; every role of a CTA walks the same sequence.
+struct Q8Walk {
+  int h = 0, r = 0, j = 0;
+  long long hi = 0;
+  bool first = true;
+
+  __device__ void skip_done(const Q8Split& S) {
+    while (h < S.H && (S.s->T[h] == 0 || j >= S.s->T[h])) {
+      j = 0;
+      if (S.s->T[h] != 0 && ++r < S.nrt) continue;
+      ++h;
+      r = 0;
+    }
+  }
+  __device__ void init(const Q8Split& S, int cta) {
+    first = true;
+    h = S.H;
+    if (S.s->total <= 0 || cta >= S.s->G) return;
+    const long long x = S.lo(cta);
+    hi = S.lo(cta + 1);
+    int a = 0, b = S.H;  // the last head with C[h] <= x
+    while (b - a > 1) {
+      const int m = (a + b) / 2;
+      if (S.s->C[m] <= x) a = m;
+      else b = m;
+    }
+    h = a;
+    r = 0;
+    j = 0;
+    if (S.s->T[h] > 0) {
+      const long long unit = static_cast<long long>(S.w) * S.s->T[h];
+      r = static_cast<int>((x - S.s->C[h]) / unit);
+      if (r > S.nrt - 1) r = S.nrt - 1;
+      const int w = S.wt(r);
+      j = static_cast<int>((x - S.start(h, r) + w - 1) / w);
+    }
+    skip_done(S);
+  }
+  __device__ bool next(const Q8Split& S, Q8Piece& pc) {
+    if (h >= S.H) return false;
+    const long long cu = S.start(h, r);
+    const int w = S.wt(r);
+    if (cu + static_cast<long long>(w) * j >= hi) return false;
+    const long long je = (hi - cu + w - 1) / w;
+    const int T = S.s->T[h];
+    pc.h = h;
+    pc.r = r;
+    pc.j0 = j;
+    pc.j1 = je < T ? static_cast<int>(je) : T;
+    q8_unit_pieces(S, h, r, pc);
+    pc.which = first ? 0 : 1;
+    first = false;
+    j = pc.j1;
+    skip_done(S);
+    return true;
+  }
+};
+
+// ------------------------------------------------------------------ launchers
+struct Q8AttendArgs {
+  Q8View c;
+  int Nq;
+  float scale;
+  const void* Q;
+  void* O;
+  float* lse;
+  float* part;  // partials: q8_part_floats(d) floats
+};
+
+struct Q8MassArgs {
+  Q8View c;
+  int Nq;
+  float scale;
+  const void* Q;
+  const float* lse;
+  float decay;
+  const float* prev;
+  float* mass;
+};
+
+cudaError_t launch_q8_attend_rows(const Q8AttendArgs& a, int n_sm, cudaStream_t st);  // bf16, 16-row tiles
+cudaError_t launch_q8_attend_f32(const Q8AttendArgs& a, int n_sm, cudaStream_t st);   // f32, CUDA cores
+cudaError_t launch_q8_mass_rows(const Q8MassArgs& a, int n_sm, cudaStream_t st);
+cudaError_t launch_q8_mass_f32(const Q8MassArgs& a, int n_sm, cudaStream_t st);
+
+// floats of partials the row-tile kernels need: two slots per CTA of 16 rows and
+// their maxima and sums
+inline size_t q8_part_floats(int d) { return static_cast<size_t>(kQ8MaxCtas) * 2 * (16 * d + 32); }
+
+struct Q8EvictArgs {
+  Q8View src;
+  const float* mass;
+  uint8_t* K;
+  uint8_t* V;
+  float* ks;
+  float* vs;
+  int* len;
+  float* to_mass;
+  int cap;  // of the destination
+  int budget, sink, recent;
+  int* kept;  // [H][budget]
+};
+cudaError_t launch_q8_evict(const Q8EvictArgs& a, cudaStream_t st);
+
+struct Q8AppendArgs {
+  int H, d, cap, block;
+  const void* X[2];  // K, V
+  long long hs[2], ts[2];
+  uint8_t* code[2];
+  float* scale[2];
+  int n;
+  const int* start;
+  int* len;
+  float* mass;
+  int* status;
+};
+cudaError_t launch_q8_append(const Q8AppendArgs& a, kvb_dtype dtype, cudaStream_t st);
+
+}  // namespace kvb

@@ -1,0 +1,218 @@
+// kvb_q8_evict: cut every head to a budget by accumulated attention weight.
+//
+// q8_select_kernel, one CTA per head: the weight of the last token to stay is found
+// digit by digit (8 bits of the order-preserving integer of a float, from the top: a
+// radix select, four passes over the head's weights, which stay in L2), then each warp
+// counts and writes the positions of its own run of tokens, so the list comes out in
+// order and of equal weights the lower positions stay.
+// q8_gather_kernel, one CTA per (block of the result, head, K or V): reads and writes
+// each kept row once.  The result's block takes the largest scale among its tokens;
+// rows from blocks of smaller scale are rounded anew (exactly scaled where both are
+// powers of two), others are copied bit for bit.
+#include "host_util.h"
+#include "q8.cuh"
+
+namespace kvb {
+namespace {
+
+constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kCopies = 8;   // histograms, so that equal digits of a warp meet less often
+
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  return w != w ? 0u : float_key(w + 0.f);  // NaN least; -0 as 0
+}
+
+__global__ void __launch_bounds__(kSelThreads) q8_select_kernel(const Q8EvictArgs a) {
+  __shared__ int hist[kCopies][256];
+  __shared__ int s_sum[256];
+  __shared__ int s_above[kSelWarps], s_equal[kSelWarps];
+  __shared__ uint32_t s_prefix;
+  __shared__ int s_need;
+  pdl_wait();
+  pdl_trigger();
+  const int h = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n = q8_len(a.src.len, h, a.src.cap);
+  int* kept = a.kept + static_cast<size_t>(h) * a.budget;
+  if (n <= a.budget) {
+    for (int i = tid; i < n; i += kSelThreads) kept[i] = i;
+    if (tid == 0) a.len[h] = n;
+    return;
+  }
+  const float* mass = a.mass + static_cast<size_t>(h) * a.src.cap;
+  const int lo = a.sink, hi = n - a.recent;
+  const int need = a.budget - a.sink - a.recent;
+  // the need-th largest key of [lo, hi): prefix of the digits found so far, and how many
+  // of the keys that share it stay
+  uint32_t thr = 0xFFFFFFFFu;
+  int quota = 0;
+  if (need > 0) {
+    if (tid == 0) {
+      s_prefix = 0u;
+      s_need = need;
+    }
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      for (int i = tid; i < kCopies * 256; i += kSelThreads) (&hist[0][0])[i] = 0;
+      __syncthreads();
+      const uint32_t prefix = s_prefix;
+      const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
+      for (int i = lo + tid; i < hi; i += kSelThreads) {
+        const uint32_t k = weight_key(__ldg(mass + i));
+        if ((k & mask) == prefix) atomicAdd(&hist[tid % kCopies][(k >> shift) & 255u], 1);
+      }
+      __syncthreads();
+      if (tid < 256) {
+        int v = 0;
+#pragma unroll
+        for (int c = 0; c < kCopies; ++c) v += hist[c][tid];
+        s_sum[tid] = v;
+      }
+      __syncthreads();
+      if (warp == 0) {
+        // keys of larger digits, eight digits a lane, from the top
+        int v[8], mine = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mine += v[k] = s_sum[255 - lane * 8 - k];
+        int above = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, above, o);
+          if (lane >= o) above += y;
+        }
+        above -= mine;
+        const int want = s_need;
+        __syncwarp();
+        if (above < want && above + mine >= want) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            if (above < want && above + v[k] >= want) {
+              s_prefix = prefix | (static_cast<uint32_t>(255 - lane * 8 - k) << shift);
+              s_need = want - above;
+            }
+            above += v[k];
+          }
+        }
+      }
+      __syncthreads();
+    }
+    thr = s_prefix;
+    quota = s_need;
+  }
+  // each warp takes one run of tokens, a multiple of 32 long
+  const int run = ((n + kSelWarps - 1) / kSelWarps + 31) & ~31;
+  const int r0 = min(warp * run, n), r1 = min(r0 + run, n);
+  auto state = [&](int i, bool& stays, bool& equal) {
+    const bool in = i < r1;
+    const bool forced = in && (i < lo || i >= hi);
+    const uint32_t k = in && !forced ? weight_key(__ldg(mass + i)) : 0u;
+    stays = forced || (in && k > thr);
+    equal = in && !forced && need > 0 && k == thr;
+  };
+  int above = 0, equal_n = 0;
+  for (int i = r0; i < r1; i += 32) {
+    bool st, eq;
+    state(i + lane, st, eq);
+    above += __popc(__ballot_sync(0xffffffffu, st));
+    equal_n += __popc(__ballot_sync(0xffffffffu, eq));
+  }
+  if (lane == 0) {
+    s_above[warp] = above;
+    s_equal[warp] = equal_n;
+  }
+  __syncthreads();
+  int at = 0, eq_before = 0;
+  for (int w = 0; w < warp; ++w) {
+    at += s_above[w];
+    eq_before += s_equal[w];
+  }
+  at += min(eq_before, quota);
+  const uint32_t below = (1u << lane) - 1u;
+  for (int i = r0; i < r1; i += 32) {
+    bool st, eq;
+    state(i + lane, st, eq);
+    const uint32_t em = __ballot_sync(0xffffffffu, eq);
+    const bool keep = st || (eq && eq_before + __popc(em & below) < quota);
+    const uint32_t km = __ballot_sync(0xffffffffu, keep);
+    if (keep) kept[at + __popc(km & below)] = i + lane;
+    at += __popc(km);
+    eq_before += __popc(em);
+  }
+  if (tid == 0) a.len[h] = a.budget;
+}
+
+constexpr int kGatherThreads = 256;
+
+// sixteen codes times r, rounded to E4M3
+__device__ __forceinline__ uint32_t rescale4(uint32_t c, float r) {
+  const float2 x = e4m3x2_to_f32x2(c), y = e4m3x2_to_f32x2(c >> 16);
+  return f32x2_to_e4m3x2(x.x * r, x.y * r) | (f32x2_to_e4m3x2(y.x * r, y.y * r) << 16);
+}
+
+__global__ void __launch_bounds__(kGatherThreads) q8_gather_kernel(const Q8EvictArgs a) {
+  __shared__ int s_src[128];
+  __shared__ float s_ratio[128];
+  __shared__ float s_max[4];
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.x, h = blockIdx.y, kv = blockIdx.z, tid = threadIdx.x;
+  const int block = a.src.block, d = a.src.d;
+  const int left = min(q8_len(a.src.len, h, a.src.cap), a.budget);
+  const int nt = min(block, left - b * block);
+  if (nt <= 0) return;
+  float sc = 0.f;
+  if (tid < 128) {
+    if (tid < nt) {
+      const int src = a.kept[static_cast<size_t>(h) * a.budget + b * block + tid];
+      s_src[tid] = src;
+      sc = (kv ? a.src.vs : a.src.ks)[static_cast<size_t>(h) * (a.src.cap / block) + src / block];
+      if (kv == 0 && a.to_mass)
+        a.to_mass[static_cast<size_t>(h) * a.cap + b * block + tid] = a.mass[static_cast<size_t>(h) * a.src.cap + src];
+    }
+    float mx = sc;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if ((tid & 31) == 0) s_max[tid >> 5] = mx;
+  }
+  __syncthreads();
+  const float to = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
+  if (tid < nt) s_ratio[tid] = sc / to;
+  __syncthreads();
+  const uint8_t* from = (kv ? a.src.V : a.src.K) + static_cast<size_t>(h) * a.src.cap * d;
+  uint4* dst = reinterpret_cast<uint4*>((kv ? a.V : a.K) + (static_cast<size_t>(h) * a.cap + b * block) * d);
+  const int words = d / 16;
+  constexpr int kFlight = 4;
+  for (int base = tid; base < nt * words; base += kGatherThreads * kFlight) {
+    uint4 w[kFlight];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      const int i = base + u * kGatherThreads;
+      if (i < nt * words)
+        w[u] = __ldg(reinterpret_cast<const uint4*>(from + static_cast<size_t>(s_src[i / words]) * d) + i % words);
+    }
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      const int i = base + u * kGatherThreads;
+      if (i >= nt * words) continue;
+      const float r = s_ratio[i / words];
+      if (r != 1.f) w[u] = make_uint4(rescale4(w[u].x, r), rescale4(w[u].y, r), rescale4(w[u].z, r), rescale4(w[u].w, r));
+      dst[i] = w[u];
+    }
+  }
+  if (tid == 0) (kv ? a.vs : a.ks)[static_cast<size_t>(h) * (a.cap / block) + b] = to;
+}
+
+}  // namespace
+
+cudaError_t launch_q8_evict(const Q8EvictArgs& a, cudaStream_t st) {
+  cudaError_t e;
+  {
+    LaunchTrace trace("q8_select_kernel", st);
+    e = launch_pdl(q8_select_kernel, dim3(a.src.H), dim3(kSelThreads), 0, st, a);
+  }
+  if (e != cudaSuccess) return e;
+  LaunchTrace trace("q8_gather_kernel", st);
+  const int blocks = (a.budget + a.src.block - 1) / a.src.block;
+  return launch_pdl(q8_gather_kernel, dim3(blocks, a.src.H, 2), dim3(kGatherThreads), 0, st, a);
+}
+
+}  // namespace kvb

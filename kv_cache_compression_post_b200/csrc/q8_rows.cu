@@ -1,0 +1,665 @@
+// Attention and attention weights over the 8-bit cache for a few rows per head: the
+// single-token form, and query heads that share a K/V head.
+//
+// Reading the cache once is the bound (2 bytes per token and channel pair), so the
+// work is split over its tokens (Q8Split), a warp takes 32 tokens at a time straight
+// from global memory into the fragments of mma.sync.m16n8k16 (16 rows x 8 tokens), and
+// no token passes through shared memory.  What the layout relies on: a contraction
+// may run over the channels, and over the tokens, in any order that both operands
+// share.  Lane (g, t) = (lane / 4, lane % 4) loads 16 contiguous bytes of token g's
+// K row and uses them as four MMA steps, so Q is fetched in that order of channels;
+// it loads 16 contiguous bytes of V for the four tokens its P columns stand for, and
+// output column n of MMA j is channel 16 n + j.  Codes widen to fp16 exactly, two per
+// instruction, and Q enters as fp16 times a power of two per row (bf16 has 8 bits,
+// fp16 11, so nothing is lost above 2^-14 of the row's largest).
+//
+// Softmax in the log2 domain.  With ks, vs the scales of a token's block,
+//     x = (q.k) ks scale log2 e,   P = 2^(x + log2 vs - m + kPBias),
+// m the running maximum of x + log2 vs: V's scale rides in the exponent at no cost,
+// P never exceeds 2^kPBias in fp16, and the row sum adds P / vs per block.  Sums,
+// maxima and partial outputs are fp32.
+#include "host_util.h"
+#include "q8.cuh"
+#include "sm100.cuh"
+
+namespace kvb {
+using namespace sm100;
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kTile = 64;    // tokens per key tile of the split
+constexpr int kSub = 32;     // tokens a warp takes at a time
+constexpr int kRows = 16;    // rows per row tile
+constexpr float kPBias = 8.f;
+constexpr int kMinTiles = 4;  // a CTA's share: one 32-token step for each warp
+
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float quad_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+
+// The A fragments of one 16-row tile: row g and g + 8 of this lane, channels 64 hb +
+// 16 t .. + 15 in the order the K bytes come.  coef[i]: what turns a raw dot product
+// of row g + 8 i into log2 units (but for the token's scale).
+template <int D>
+struct QFrag {
+  uint32_t a[D / 16][4];
+  float coef[2];
+
+  __device__ __forceinline__ void load(const __nv_bfloat16* Q, int rows, float scale, int g, int t) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = g + 8 * i;
+      uint4 w[D / 32];
+#pragma unroll
+      for (int hb = 0; hb < D / 64; ++hb)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          w[hb * 2 + k] = row < rows ? *(reinterpret_cast<const uint4*>(Q + static_cast<size_t>(row) * D + hb * 64 + t * 16) + k)
+                                     : make_uint4(0u, 0u, 0u, 0u);
+      float mx = 0.f;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = unpack_bf16x2(u[e]);
+          if (fabsf(f.x) <= 3.4e38f) mx = fmaxf(mx, fabsf(f.x));
+          if (fabsf(f.y) <= 3.4e38f) mx = fmaxf(mx, fabsf(f.y));
+        }
+      }
+      mx = quad_max(mx);
+      const int e = min(max(exponent_of(mx), -100), 126);
+      const float down = pow2f(-e);
+      coef[i] = pow2f(e) * scale * kLog2e;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        // 8 channels: two MMA steps, (0,1) and (2,3) of each to registers i, i + 2
+        const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+        for (int e2 = 0; e2 < 4; ++e2) {
+          const float2 f = unpack_bf16x2(u[e2]);
+          a[k * 2 + (e2 >> 1)][i + 2 * (e2 & 1)] = pack_f16x2(f.x * down, f.y * down);
+        }
+      }
+    }
+  }
+};
+
+// Raw K words of 32 tokens from `kb` (token index in the head), rows past the last
+// held token read the last one (masked later).
+template <int D>
+struct KWords {
+  uint4 w[4][D / 64];
+  __device__ __forceinline__ void load(const uint8_t* K, int kb, int last, int g, int t) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int key = min(kb + 8 * j + g, last);
+#pragma unroll
+      for (int hb = 0; hb < D / 64; ++hb)
+        w[j][hb] = __ldg(reinterpret_cast<const uint4*>(K + static_cast<size_t>(key) * D + hb * 64 + t * 16));
+    }
+  }
+  // s[j]: raw dot products of rows g (0, 1) and g + 8 (2, 3) with tokens 8 j + 2 t, + 1
+  __device__ __forceinline__ void dots(const QFrag<D>& q, float (&s)[4][4]) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[j][k] = 0.f;
+#pragma unroll
+      for (int hb = 0; hb < D / 64; ++hb) {
+        const uint32_t u[4] = {w[j][hb].x, w[j][hb].y, w[j][hb].z, w[j][hb].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mma_16816(s[j], q.a[hb * 4 + i], e4m3x2_to_f16x2(u[i]), e4m3x2_to_f16x2(u[i] >> 16));
+      }
+    }
+  }
+};
+
+template <int D>
+struct VWords {
+  static constexpr int kW = D / 32;  // 32-bit words per lane and token (8 lanes per row)
+  uint32_t w[2][4][kW];
+  __device__ __forceinline__ void load(const uint8_t* V, int kb, int last, int g, int t) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int key = min(kb + 16 * u + 2 * t + (k & 1) + 8 * (k >> 1), last);
+        const uint8_t* p = V + static_cast<size_t>(key) * D + g * (D / 8);
+        if constexpr (D == 128) {
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
+          w[u][k][0] = x.x, w[u][k][1] = x.y, w[u][k][2] = x.z, w[u][k][3] = x.w;
+        } else {
+          const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+          w[u][k][0] = x.x, w[u][k][1] = x.y;
+        }
+      }
+  }
+  // o[j] += P[16 tokens of half u] V, channel (D / 8) n + j in column n
+  __device__ __forceinline__ void accumulate(int u, const uint32_t (&p)[4], float (&o)[D / 8][4]) const {
+#pragma unroll
+    for (int q = 0; q < kW; ++q) {
+      const uint32_t a0 = __byte_perm(w[u][0][q], w[u][1][q], 0x5140), a1 = __byte_perm(w[u][0][q], w[u][1][q], 0x7362);
+      const uint32_t b0 = __byte_perm(w[u][2][q], w[u][3][q], 0x5140), b1 = __byte_perm(w[u][2][q], w[u][3][q], 0x7362);
+      mma_16816(o[4 * q + 0], p, e4m3x2_to_f16x2(a0), e4m3x2_to_f16x2(b0));
+      mma_16816(o[4 * q + 1], p, e4m3x2_to_f16x2(a0 >> 16), e4m3x2_to_f16x2(b0 >> 16));
+      mma_16816(o[4 * q + 2], p, e4m3x2_to_f16x2(a1), e4m3x2_to_f16x2(b1));
+      mma_16816(o[4 * q + 3], p, e4m3x2_to_f16x2(a1 >> 16), e4m3x2_to_f16x2(b1 >> 16));
+    }
+  }
+};
+
+template <int D>
+constexpr size_t slot_floats() { return static_cast<size_t>(kRows) * D + 2 * kRows; }
+
+// what the eight warps of a CTA leave for their merge
+template <int D>
+struct RowsShared {
+  float o[kWarps][kRows][D + 4];
+  float m[kWarps][kRows], l[kWarps][kRows];
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) q8_attend_rows_kernel(const Q8AttendArgs a) {
+  extern __shared__ uint8_t smem[];
+  __shared__ Q8Sched sch;
+  RowsShared<D>& sh = *reinterpret_cast<RowsShared<D>*>(smem);
+  pdl_wait();
+  pdl_trigger();
+  const int nrt = (a.Nq + kRows - 1) / kRows;
+  q8_build_sched(&sch, a.c.len, a.c.cap, a.c.H, nrt, kTile, 1, 1, gridDim.x, kMinTiles);
+  Q8Split S{&sch, a.c.H, nrt, 1, 1};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int blocks = a.c.cap / a.c.block;
+  Q8Walk walk;
+  walk.init(S, blockIdx.x);
+  Q8Piece pc;
+  while (walk.next(S, pc)) {
+    const int n = q8_len(a.c.len, pc.h, a.c.cap);
+    const int end = min(pc.j1 * kTile, n);
+    const int rows = min(kRows, a.Nq - pc.r * kRows);
+    const size_t row0 = static_cast<size_t>(pc.h) * a.Nq + pc.r * kRows;
+    const uint8_t* K = a.c.K + static_cast<size_t>(pc.h) * a.c.cap * D;
+    const uint8_t* V = a.c.V + static_cast<size_t>(pc.h) * a.c.cap * D;
+    const float* ks = a.c.ks + static_cast<size_t>(pc.h) * blocks;
+    const float* vs = a.c.vs + static_cast<size_t>(pc.h) * blocks;
+    QFrag<D> q;
+    q.load(static_cast<const __nv_bfloat16*>(a.Q) + row0 * D, rows, a.scale, g, t);
+    float o[D / 8][4];
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[j][k] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    for (int kb = pc.j0 * kTile + warp * kSub; kb < end; kb += kWarps * kSub) {
+      KWords<D> kw;
+      VWords<D> vw;
+      kw.load(K, kb, n - 1, g, t);
+      vw.load(V, kb, n - 1, g, t);
+      float kf[2], lv[2], iv[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int b = min(kb + 16 * u, n - 1) / a.c.block;
+        const float v = __ldg(vs + b);
+        kf[u] = __ldg(ks + b);
+        lv[u] = log2f(v);
+        iv[u] = 1.f / v;
+      }
+      float s[4][4];
+      kw.dots(q, s);
+      float mt[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int key = kb + 8 * j + 2 * t + (k & 1);
+          const float x = fmaf(s[j][k], q.coef[k >> 1] * kf[j >> 1], lv[j >> 1]);
+          s[j][k] = key < end ? x : -INFINITY;
+          mt[k >> 1] = fmaxf(mt[k >> 1], s[j][k]);
+        }
+      mt[0] = quad_max(mt[0]);
+      mt[1] = quad_max(mt[1]);
+      if (__any_sync(0xffffffffu, mt[0] > m[0] || mt[1] > m[1])) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float mn = fmaxf(m[i], mt[i]);
+          const float al = mn == -INFINITY ? 1.f : exp2f(m[i] - mn);
+          m[i] = mn;
+          l[i] *= al;
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j) {
+            o[j][2 * i] *= al;
+            o[j][2 * i + 1] *= al;
+          }
+        }
+      }
+      // a row whose every score is -inf so far (NaN queries aside) keeps P = 0
+      const float b0 = (m[0] == -INFINITY ? 0.f : -m[0]) + kPBias, b1 = (m[1] == -INFINITY ? 0.f : -m[1]) + kPBias;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float r0 = 0.f, r1 = 0.f;
+        uint32_t p[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int j = 2 * u + i;
+          const float p0 = ex2_approx(s[j][0] + b0), p1 = ex2_approx(s[j][1] + b0);
+          const float p2 = ex2_approx(s[j][2] + b1), p3 = ex2_approx(s[j][3] + b1);
+          r0 += p0 + p1;
+          r1 += p2 + p3;
+          p[2 * i] = pack_f16x2(p0, p1);
+          p[2 * i + 1] = pack_f16x2(p2, p3);
+        }
+        l[0] = fmaf(r0, iv[u], l[0]);
+        l[1] = fmaf(r1, iv[u], l[1]);
+        vw.accumulate(u, p, o);
+      }
+    }
+    // merge the eight warps: maxima first, then every output weighted by its warp
+    l[0] = quad_sum(l[0]);
+    l[1] = quad_sum(l[1]);
+    __syncthreads();  // the previous piece's merge is done with the shared memory
+    if (t == 0) {
+      sh.m[warp][g] = m[0], sh.m[warp][g + 8] = m[1];
+      sh.l[warp][g] = l[0], sh.l[warp][g + 8] = l[1];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int row = g + 8 * (k >> 1);
+      if (row >= rows) continue;
+      float* to = &sh.o[warp][row][(2 * t + (k & 1)) * (D / 8)];
+#pragma unroll
+      for (int j = 0; j < D / 8; j += 4)
+        *reinterpret_cast<float4*>(to + j) = make_float4(o[j][k], o[j + 1][k], o[j + 2][k], o[j + 3][k]);
+    }
+    __syncthreads();
+    float* slot = a.part + static_cast<size_t>(blockIdx.x * 2 + pc.which) * slot_floats<D>();
+    for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
+      const int row = i / (D / 4), c = (i % (D / 4)) * 4;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sh.m[w][row]);
+      float L = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = M == -INFINITY ? 1.f : exp2f(sh.m[w][row] - M);
+        const float4 x = *reinterpret_cast<const float4*>(&sh.o[w][row][c]);
+        L = fmaf(f, sh.l[w][row], L);
+        acc.x = fmaf(f, x.x, acc.x);
+        acc.y = fmaf(f, x.y, acc.y);
+        acc.z = fmaf(f, x.z, acc.z);
+        acc.w = fmaf(f, x.w, acc.w);
+      }
+      if (pc.npieces == 1) {
+        const float inv = 1.f / L;
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + (row0 + row) * D + c) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        if (a.lse && c == 0) a.lse[row0 + row] = (M - kPBias + log2f(L)) * kLn2;
+      } else {
+        *reinterpret_cast<float4*>(slot + row * D + c) = acc;
+        if (c == 0) {
+          slot[kRows * D + row] = M;
+          slot[kRows * D + kRows + row] = L;
+        }
+      }
+    }
+  }
+}
+
+// Units cut into pieces, and heads without tokens: one CTA per (row tile, head).
+// Every CTA lays out the same split again (the lengths have not changed).
+template <int D, typename T>
+__global__ void __launch_bounds__(128) q8_merge_rows_kernel(const Q8AttendArgs a, int tile_rows, int tile, int grid,
+                                                           int min_tiles, float bias) {
+  __shared__ Q8Sched sch;
+  pdl_wait();
+  pdl_trigger();
+  const int nrt = (a.Nq + tile_rows - 1) / tile_rows;
+  q8_build_sched(&sch, a.c.len, a.c.cap, a.c.H, nrt, tile, 1, 1, grid, min_tiles);
+  Q8Split S{&sch, a.c.H, nrt, 1, 1};
+  const int r = blockIdx.x, h = blockIdx.y;
+  const int rows = min(tile_rows, a.Nq - r * tile_rows);
+  const size_t row0 = static_cast<size_t>(h) * a.Nq + r * tile_rows;
+  const size_t slot_size = static_cast<size_t>(kRows) * D + 2 * kRows;
+  T* O = static_cast<T*>(a.O);
+  auto put = [&](int row, int c, float4 v) {
+    T* p = O + (row0 + row) * D + c;
+    if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    else *reinterpret_cast<float4*>(p) = v;
+  };
+  Q8Piece pc;
+  const bool empty = sch.T[h] == 0;
+  if (!empty) {
+    q8_unit_pieces(S, h, r, pc);
+    if (pc.npieces == 1) return;
+  }
+  for (int i = threadIdx.x; i < rows * (D / 4); i += blockDim.x) {
+    const int row = i / (D / 4), c = (i % (D / 4)) * 4;
+    if (empty) {
+      put(row, c, make_float4(0.f, 0.f, 0.f, 0.f));
+      if (a.lse && c == 0) a.lse[row0 + row] = -INFINITY;
+      continue;
+    }
+    float M = -INFINITY;
+    for (int k = 0; k < pc.npieces; ++k) {
+      const float* s = a.part + static_cast<size_t>((pc.cfirst + k) * 2 + (k ? 0 : pc.wfirst)) * slot_size;
+      M = fmaxf(M, s[kRows * D + row]);
+    }
+    float L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < pc.npieces; ++k) {
+      const float* s = a.part + static_cast<size_t>((pc.cfirst + k) * 2 + (k ? 0 : pc.wfirst)) * slot_size;
+      const float f = M == -INFINITY ? 1.f : exp2f(s[kRows * D + row] - M);
+      const float4 x = *reinterpret_cast<const float4*>(s + row * D + c);
+      L = fmaf(f, s[kRows * D + kRows + row], L);
+      acc.x = fmaf(f, x.x, acc.x);
+      acc.y = fmaf(f, x.y, acc.y);
+      acc.z = fmaf(f, x.z, acc.z);
+      acc.w = fmaf(f, x.w, acc.w);
+    }
+    const float inv = 1.f / L;
+    put(row, c, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    if (a.lse && c == 0) a.lse[row0 + row] = (M - bias + log2f(L)) * kLn2;
+  }
+}
+
+// ------------------------------------------------------------------ f32 rows
+// Queries and outputs of 32 bits keep 24-bit products: CUDA cores, kF32Rows rows at a
+// time.  Eight lanes share a token (D / 8 channels each), so a warp works through four
+// tokens side by side, each group of lanes with its own running maximum.
+constexpr int kF32Rows = 4;
+constexpr int kF32Threads = 128;
+constexpr int kF32Groups = kF32Threads / 8;
+
+template <int D>
+__device__ __forceinline__ void load_codes(const uint8_t* p, float (&f)[D / 8]) {
+  uint32_t w[D / 32];
+  if constexpr (D == 128) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+  } else {
+    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+    w[0] = x.x, w[1] = x.y;
+  }
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) {
+    const float2 a = e4m3x2_to_f32x2(w[k]), b = e4m3x2_to_f32x2(w[k] >> 16);
+    f[4 * k] = a.x, f[4 * k + 1] = a.y, f[4 * k + 2] = b.x, f[4 * k + 3] = b.y;
+  }
+}
+template <int D>
+__device__ __forceinline__ void load_q(const float* p, float mul, float (&f)[D / 8]) {
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) {
+    const float4 x = *(reinterpret_cast<const float4*>(p) + k);
+    f[4 * k] = x.x * mul, f[4 * k + 1] = x.y * mul, f[4 * k + 2] = x.z * mul, f[4 * k + 3] = x.w * mul;
+  }
+}
+__device__ __forceinline__ float octet_sum(float v) {
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kF32Threads) q8_attend_f32_kernel(const Q8AttendArgs a) {
+  extern __shared__ uint8_t smem[];
+  __shared__ Q8Sched sch;
+  __shared__ float sm[kF32Groups][kF32Rows], sl[kF32Groups][kF32Rows];
+  float* so = reinterpret_cast<float*>(smem);  // [group][row][D]
+  pdl_wait();
+  pdl_trigger();
+  const int nrt = (a.Nq + kF32Rows - 1) / kF32Rows;
+  q8_build_sched(&sch, a.c.len, a.c.cap, a.c.H, nrt, kTile, 1, 1, gridDim.x, kMinTiles);
+  Q8Split S{&sch, a.c.H, nrt, 1, 1};
+  const int grp = threadIdx.x >> 3, sub = threadIdx.x & 7;
+  const int blocks = a.c.cap / a.c.block;
+  Q8Walk walk;
+  walk.init(S, blockIdx.x);
+  Q8Piece pc;
+  while (walk.next(S, pc)) {
+    const int n = q8_len(a.c.len, pc.h, a.c.cap);
+    const int end = min(pc.j1 * kTile, n);
+    const int rows = min(kF32Rows, a.Nq - pc.r * kF32Rows);
+    const size_t row0 = static_cast<size_t>(pc.h) * a.Nq + pc.r * kF32Rows;
+    const size_t at = static_cast<size_t>(pc.h) * a.c.cap * D + sub * (D / 8);
+    float q[kF32Rows][D / 8], acc[kF32Rows][D / 8], m[kF32Rows], l[kF32Rows];
+#pragma unroll
+    for (int r = 0; r < kF32Rows; ++r) {
+      load_q<D>(static_cast<const float*>(a.Q) + (row0 + min(r, rows - 1)) * D + sub * (D / 8), a.scale * kLog2e, q[r]);
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k) acc[r][k] = 0.f;
+    }
+    // whole warps take the same number of steps, so that the sums can shuffle
+    const int first = pc.j0 * kTile;
+    const int steps = (end - first + kF32Groups - 1) / kF32Groups;
+    for (int i = 0; i < steps; ++i) {
+      const int key = first + i * kF32Groups + grp;
+      const int kc = min(key, end - 1);
+      float kf[D / 8], vf[D / 8];
+      load_codes<D>(a.c.K + at + static_cast<size_t>(kc) * D, kf);
+      load_codes<D>(a.c.V + at + static_cast<size_t>(kc) * D, vf);
+      const float ks = __ldg(a.c.ks + static_cast<size_t>(pc.h) * blocks + kc / a.c.block);
+      const float vs = __ldg(a.c.vs + static_cast<size_t>(pc.h) * blocks + kc / a.c.block);
+#pragma unroll
+      for (int r = 0; r < kF32Rows; ++r) {
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) s = fmaf(q[r][k], kf[k], s);
+        const float dot = octet_sum(s);
+        const float x = key < end ? dot * ks : -INFINITY;
+        if (x > m[r]) {
+          const float al = exp2f(m[r] - x);
+          m[r] = x;
+          l[r] *= al;
+#pragma unroll
+          for (int k = 0; k < D / 8; ++k) acc[r][k] *= al;
+        }
+        const float p = key < end ? exp2f(x - m[r]) : 0.f;
+        l[r] += p;
+        const float pv = p * vs;
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) acc[r][k] = fmaf(pv, vf[k], acc[r][k]);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kF32Rows; ++r) {
+      if (sub == 0) sm[grp][r] = m[r], sl[grp][r] = l[r];
+#pragma unroll
+      for (int k = 0; k < D / 8; k += 4)
+        *reinterpret_cast<float4*>(so + (static_cast<size_t>(grp) * kF32Rows + r) * D + sub * (D / 8) + k) =
+            make_float4(acc[r][k], acc[r][k + 1], acc[r][k + 2], acc[r][k + 3]);
+    }
+    __syncthreads();
+    float* slot = a.part + static_cast<size_t>(blockIdx.x * 2 + pc.which) * slot_floats<D>();
+    for (int i = threadIdx.x; i < rows * D; i += kF32Threads) {
+      const int row = i / D, c = i % D;
+      float M = -INFINITY;
+      for (int w = 0; w < kF32Groups; ++w) M = fmaxf(M, sm[w][row]);
+      float L = 0.f, v = 0.f;
+      for (int w = 0; w < kF32Groups; ++w) {
+        const float f = M == -INFINITY ? 1.f : exp2f(sm[w][row] - M);
+        L = fmaf(f, sl[w][row], L);
+        v = fmaf(f, so[(static_cast<size_t>(w) * kF32Rows + row) * D + c], v);
+      }
+      if (pc.npieces == 1) {
+        static_cast<float*>(a.O)[(row0 + row) * D + c] = v / L;
+        if (a.lse && c == 0) a.lse[row0 + row] = (M + log2f(L)) * kLn2;
+      } else {
+        slot[row * D + c] = v;
+        if (c == 0) {
+          slot[kRows * D + row] = M;
+          slot[kRows * D + kRows + row] = L;
+        }
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ weights
+// mass[k] = decay prev[k] + sum over rows of 2^(x - lse log2 e): a token's weight is
+// whole within its warp, so there is nothing to split or merge, and the rows are added
+// in one fixed order.  Reads K once per 16 rows (the first time from memory).
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) q8_mass_rows_kernel(const Q8MassArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int h = blockIdx.y;
+  const int n = q8_len(a.c.len, h, a.c.cap);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const uint8_t* K = a.c.K + static_cast<size_t>(h) * a.c.cap * D;
+  const float* ks = a.c.ks + static_cast<size_t>(h) * (a.c.cap / a.c.block);
+  for (int kb = (blockIdx.x * kWarps + warp) * kSub; kb < n; kb += gridDim.x * kWarps * kSub) {
+    KWords<D> kw;
+    kw.load(K, kb, n - 1, g, t);
+    float kf[2], w[4][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) kf[u] = __ldg(ks + min(kb + 16 * u, n - 1) / a.c.block);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j][0] = w[j][1] = 0.f;
+    for (int r0 = 0; r0 < a.Nq; r0 += kRows) {
+      const size_t row0 = static_cast<size_t>(h) * a.Nq + r0;
+      const int rows = min(kRows, a.Nq - r0);
+      QFrag<D> q;
+      q.load(static_cast<const __nv_bfloat16*>(a.Q) + row0 * D, rows, a.scale, g, t);
+      float z[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float v = g + 8 * i < rows ? a.lse[row0 + g + 8 * i] : -INFINITY;
+        z[i] = v == -INFINITY ? -INFINITY : -v * kLog2e;  // a row of lse -inf weighs nothing
+      }
+      float s[4][4];
+      kw.dots(q, s);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[j][k & 1] += ex2_approx(fmaf(s[j][k], q.coef[k >> 1] * kf[j >> 1], z[k >> 1]));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float v = w[j][i];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        const int key = kb + 8 * j + 2 * t + i;
+        if (g == 2 * j + i && key < n) {
+          const size_t at = static_cast<size_t>(h) * a.c.cap + key;
+          a.mass[at] = a.prev ? fmaf(a.decay, a.prev[at], v) : v;
+        }
+      }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) q8_mass_f32_kernel(const Q8MassArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int h = blockIdx.y;
+  const int n = q8_len(a.c.len, h, a.c.cap);
+  const int grp = threadIdx.x >> 3, sub = threadIdx.x & 7;
+  constexpr int kGroups = kThreads / 8;
+  const int base = blockIdx.x * kGroups;
+  for (int k0 = base; k0 < n; k0 += gridDim.x * kGroups) {
+    const int key = k0 + grp, kc = min(key, n - 1);
+    float kf[D / 8];
+    load_codes<D>(a.c.K + (static_cast<size_t>(h) * a.c.cap + kc) * D + sub * (D / 8), kf);
+    const float mul = __ldg(a.c.ks + static_cast<size_t>(h) * (a.c.cap / a.c.block) + kc / a.c.block) * a.scale;
+    float w = 0.f;
+    for (int r = 0; r < a.Nq; ++r) {
+      const size_t row = static_cast<size_t>(h) * a.Nq + r;
+      float q[D / 8];
+      load_q<D>(static_cast<const float*>(a.Q) + row * D + sub * (D / 8), 1.f, q);
+      float s = 0.f;
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k) s = fmaf(q[k], kf[k], s);
+      const float z = a.lse[row];
+      const float x = octet_sum(s);
+      if (z != -INFINITY) w += expf(fmaf(x, mul, -z));
+    }
+    if (sub == 0 && key < n) {
+      const size_t at = static_cast<size_t>(h) * a.c.cap + key;
+      a.mass[at] = a.prev ? fmaf(a.decay, a.prev[at], w) : w;
+    }
+  }
+}
+
+int split_grid(int n_sm) { return n_sm < kQ8MaxCtas ? n_sm : kQ8MaxCtas; }
+
+template <int D>
+cudaError_t attend_rows(const Q8AttendArgs& a, int n_sm, cudaStream_t st) {
+  const int grid = split_grid(n_sm);
+  cudaError_t e = cudaFuncSetAttribute(q8_attend_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(sizeof(RowsShared<D>)));
+  if (e != cudaSuccess) return e;
+  {
+    LaunchTrace trace("q8_attend_rows_kernel", st);
+    e = launch_pdl(q8_attend_rows_kernel<D>, dim3(grid), dim3(kThreads), sizeof(RowsShared<D>), st, a);
+  }
+  if (e != cudaSuccess) return e;
+  LaunchTrace trace("q8_merge_rows_kernel", st);
+  return launch_pdl(q8_merge_rows_kernel<D, __nv_bfloat16>, dim3((a.Nq + kRows - 1) / kRows, a.c.H), dim3(128), 0, st, a,
+                    static_cast<int>(kRows), static_cast<int>(kTile), grid, static_cast<int>(kMinTiles), static_cast<float>(kPBias));
+}
+
+template <int D>
+cudaError_t attend_f32(const Q8AttendArgs& a, int n_sm, cudaStream_t st) {
+  const int grid = split_grid(n_sm);
+  const size_t smem = static_cast<size_t>(kF32Groups) * kF32Rows * D * sizeof(float);
+  cudaError_t e;
+  {
+    LaunchTrace trace("q8_attend_f32_kernel", st);
+    e = launch_pdl(q8_attend_f32_kernel<D>, dim3(grid), dim3(kF32Threads), smem, st, a);
+  }
+  if (e != cudaSuccess) return e;
+  LaunchTrace trace("q8_merge_rows_kernel", st);
+  return launch_pdl(q8_merge_rows_kernel<D, float>, dim3((a.Nq + kF32Rows - 1) / kF32Rows, a.c.H), dim3(128), 0, st, a,
+                    static_cast<int>(kF32Rows), static_cast<int>(kTile), grid, static_cast<int>(kMinTiles), 0.f);
+}
+
+// CTAs per head so that the grid is about `waves` waves, no more than the tokens need
+int mass_blocks(int cap, int per_cta, int H, int n_sm, int waves) {
+  const int need = (cap + per_cta - 1) / per_cta;
+  const int room = (n_sm * waves + H - 1) / H;
+  return need < room ? need : (room < 1 ? 1 : room);
+}
+
+}  // namespace
+
+cudaError_t launch_q8_attend_rows(const Q8AttendArgs& a, int n_sm, cudaStream_t st) {
+  return a.c.d == 128 ? attend_rows<128>(a, n_sm, st) : attend_rows<64>(a, n_sm, st);
+}
+cudaError_t launch_q8_attend_f32(const Q8AttendArgs& a, int n_sm, cudaStream_t st) {
+  return a.c.d == 128 ? attend_f32<128>(a, n_sm, st) : attend_f32<64>(a, n_sm, st);
+}
+cudaError_t launch_q8_mass_rows(const Q8MassArgs& a, int n_sm, cudaStream_t st) {
+  const dim3 grid(mass_blocks(a.c.cap, kWarps * kSub, a.c.H, n_sm, 2), a.c.H);
+  LaunchTrace trace("q8_mass_rows_kernel", st);
+  return a.c.d == 128 ? launch_pdl(q8_mass_rows_kernel<128>, grid, dim3(kThreads), 0, st, a)
+                      : launch_pdl(q8_mass_rows_kernel<64>, grid, dim3(kThreads), 0, st, a);
+}
+cudaError_t launch_q8_mass_f32(const Q8MassArgs& a, int n_sm, cudaStream_t st) {
+  const dim3 grid(mass_blocks(a.c.cap, kThreads / 8, a.c.H, n_sm, 8), a.c.H);
+  LaunchTrace trace("q8_mass_f32_kernel", st);
+  return a.c.d == 128 ? launch_pdl(q8_mass_f32_kernel<128>, grid, dim3(kThreads), 0, st, a)
+                      : launch_pdl(q8_mass_f32_kernel<64>, grid, dim3(kThreads), 0, st, a);
+}
+
+}  // namespace kvb

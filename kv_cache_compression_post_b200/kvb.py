@@ -23,6 +23,8 @@ __all__ = [
     "kvb_attend", "kvb_read_stats", "kvb_bank_export", "kvb_bank_import", "kvb_device_status",
     "kvb_status_string", "kvb_launch_count", "kvb_trace_enable", "kvb_trace_read", "kvb_density_workspace_size", "kvb_density", "kvb_density_noalloc", "kvb_segment_cosine",
     "kvb_selftest_timeout", "kvb_admit_begin", "kvb_admit_finish",
+    "KVB_ROPE_INTERLEAVED", "KVB_ROPE_HALVES", "kvb_rope", "rope",
+    "kvb_q8_cache", "kvb_q8_workspace_size", "kvb_q8_append", "kvb_q8_attend", "kvb_q8_mass", "kvb_q8_evict", "Q8Cache",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkvb.so")
@@ -35,6 +37,7 @@ KVB_EVICT_THRESHOLD_RATIO, KVB_EVICT_DENSEST, KVB_EVICT_THRESHOLD_SOURCE = 0, 1,
 KVB_BOTTOMK_FRAME, KVB_BOTTOMK_CALL = 0, 1
 KVB_SIM_PER_LAYER, KVB_SIM_FIRST_LAYER = 0, 1
 KVB_STORE_NATIVE, KVB_STORE_FP8_E4M3 = 0, 1
+KVB_ROPE_INTERLEAVED, KVB_ROPE_HALVES = 0, 1
 
 # The Soft-Riesz parameters the DensityKV pages select (§4 parameter sensitivity,
 # App. E parameter sweeps: width sigma = 8, decay p = 2, regulariser eps fixed
@@ -92,12 +95,20 @@ class kvb_trace_record(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_char_p), ("ms", ctypes.c_float), ("device", ctypes.c_int32)]
 
 
+class kvb_q8_cache(ctypes.Structure):
+    _fields_ = [("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("capacity", ctypes.c_int32),
+                ("block", ctypes.c_int32), ("K", ctypes.c_void_p), ("V", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("len", ctypes.c_void_p),
+                ("mass", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with `python -m kv_cache_compression_post_b200.build`")
 
 lib = ctypes.CDLL(LIB_PATH)
 
 _vp, _i32, _f, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
+_i64, _q8 = ctypes.c_int64, ctypes.POINTER(kvb_q8_cache)
 _SIGS = {
     "kvb_workspace_size": (_sz, [ctypes.POINTER(kvb_config)]),
     "kvb_bank_create": (ctypes.c_int, [ctypes.POINTER(kvb_config), _vp, _sz, _vp, ctypes.POINTER(_vp)]),
@@ -123,6 +134,13 @@ _SIGS = {
     "kvb_selftest_timeout": (ctypes.c_int, [_vp, _vp, ctypes.c_int64, _vp]),
     "kvb_admit_begin": (ctypes.c_int, [_vp, _i32, _vp, _vp, _vp, _i32, _vp, _vp]),
     "kvb_admit_finish": (ctypes.c_int, [_vp, _i32, _vp, _vp]),
+    "kvb_rope": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i32, ctypes.c_int, ctypes.POINTER(_i32), _f, ctypes.c_int, _i32,
+                                _i64, _i64, _vp, _i64, _i64, _vp]),
+    "kvb_q8_workspace_size": (_sz, [_q8, _i32, ctypes.c_int]),
+    "kvb_q8_append": (ctypes.c_int, [_q8, _vp, _i64, _i64, _vp, _i64, _i64, _i32, ctypes.c_int, _vp, _vp]),
+    "kvb_q8_attend": (ctypes.c_int, [_q8, _vp, _i32, ctypes.c_int, _f, _vp, _vp, _vp, _sz, _vp]),
+    "kvb_q8_mass": (ctypes.c_int, [_q8, _vp, _i32, ctypes.c_int, _f, _vp, _f, _vp, _vp, _sz, _vp]),
+    "kvb_q8_evict": (ctypes.c_int, [_q8, _q8, _i32, _i32, _i32, _vp, _vp, _sz, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(lib, _name)
@@ -274,6 +292,167 @@ def kvb_segment_cosine(K, nextK, heads: int, n_frames: int, frame_h: int, frame_
                        head_dim: int, dtype: int, sim, stream=None) -> None:
     _check(lib.kvb_segment_cosine(_ptr(K), _ptr(nextK), heads, n_frames, frame_h, frame_w, seg_h, seg_w, head_dim,
                                   dtype, _ptr(sim), _stream(stream)), "kvb_segment_cosine")
+
+
+def kvb_rope(X, pos, heads: int, n_tokens: int, head_dim: int, dtype: int, axis_pairs, base: float, pairing: int,
+             inverse: int, x_head_stride: int, x_token_stride: int, out, out_head_stride: int, out_token_stride: int,
+             stream=None) -> None:
+    """axis_pairs: three host integers."""
+    _check(lib.kvb_rope(_ptr(X), _ptr(pos), heads, n_tokens, head_dim, dtype, (_i32 * 3)(*axis_pairs), base, pairing,
+                        inverse, x_head_stride, x_token_stride, _ptr(out), out_head_stride, out_token_stride,
+                        _stream(stream)), "kvb_rope")
+
+
+def kvb_q8_workspace_size(cache: kvb_q8_cache, max_queries: int, dtype: int) -> int:
+    return lib.kvb_q8_workspace_size(ctypes.byref(cache), max_queries, dtype)
+
+
+def kvb_q8_append(cache: kvb_q8_cache, K, k_head_stride: int, k_token_stride: int, V, v_head_stride: int,
+                  v_token_stride: int, n: int, dtype: int, start=None, stream=None) -> None:
+    _check(lib.kvb_q8_append(ctypes.byref(cache), _ptr(K), k_head_stride, k_token_stride, _ptr(V), v_head_stride,
+                             v_token_stride, n, dtype, _ptr(start), _stream(stream)), "kvb_q8_append")
+
+
+def kvb_q8_attend(cache: kvb_q8_cache, Q, Nq: int, dtype: int, scale: float, O, lse, workspace, workspace_bytes: int,
+                  stream=None) -> None:
+    _check(lib.kvb_q8_attend(ctypes.byref(cache), _ptr(Q), Nq, dtype, scale, _ptr(O), _ptr(lse), _ptr(workspace),
+                             workspace_bytes, _stream(stream)), "kvb_q8_attend")
+
+
+def kvb_q8_mass(cache: kvb_q8_cache, Q, Nq: int, dtype: int, scale: float, lse, decay: float, prev, workspace,
+                workspace_bytes: int, stream=None) -> None:
+    _check(lib.kvb_q8_mass(ctypes.byref(cache), _ptr(Q), Nq, dtype, scale, _ptr(lse), decay, _ptr(prev),
+                           _ptr(workspace), workspace_bytes, _stream(stream)), "kvb_q8_mass")
+
+
+def kvb_q8_evict(src: kvb_q8_cache, dst: kvb_q8_cache, budget: int, sink: int, recent: int, kept, workspace,
+                 workspace_bytes: int, stream=None) -> None:
+    _check(lib.kvb_q8_evict(ctypes.byref(src), ctypes.byref(dst), budget, sink, recent, _ptr(kept), _ptr(workspace),
+                            workspace_bytes, _stream(stream)), "kvb_q8_evict")
+
+
+def _tensor_dtype(x, where: str) -> int:
+    import torch
+    if x.dtype == torch.bfloat16:
+        return KVB_BF16
+    if x.dtype == torch.float32:
+        return KVB_F32
+    raise KvbError(1, where)
+
+
+def _rows(x, shape, dtype: int, where: str):
+    """A [heads][n][d] tensor of a call, in any order of its rows: its head and token
+    strides, after checking its shape, its type and that a row is contiguous."""
+    if tuple(x.shape) != tuple(shape) or _tensor_dtype(x, where) != dtype or not x.is_cuda or \
+            (x.stride(2) != 1 and shape[2] != 1):
+        raise KvbError(1, where)
+    # the stride of a dimension of one row says nothing
+    return (x.stride(0) if shape[0] > 1 else 0), (x.stride(1) if shape[1] > 1 else 0)
+
+
+def _whole(x, shape, dtype, where: str) -> None:
+    """A contiguous device tensor of a call (None passes)."""
+    if x is not None and (tuple(x.shape) != tuple(shape) or x.dtype != dtype or not x.is_cuda or
+                          not x.is_contiguous()):
+        raise KvbError(1, where)
+
+
+def rope(X, pos, out, axis_pairs, base: float = 10000.0, pairing: int = KVB_ROPE_INTERLEAVED, inverse: bool = False,
+         stream=None) -> None:
+    """kvb_rope on [heads][tokens][d] views of any row order (``x.transpose(0, 1)`` of a
+    token-major tensor, say), both of one type; pos int32 [tokens][3]."""
+    import torch
+    dtype = _tensor_dtype(X, "kvb_rope")
+    if X.dim() != 3:
+        raise KvbError(1, "kvb_rope")
+    h, n, d = X.shape
+    xs = _rows(X, (h, n, d), dtype, "kvb_rope")
+    os_ = _rows(out, (h, n, d), dtype, "kvb_rope")
+    _whole(pos, (n, 3), torch.int32, "kvb_rope")
+    kvb_rope(X, pos, h, n, d, dtype, axis_pairs, base, pairing, 1 if inverse else 0, xs[0], xs[1], out, os_[0], os_[1],
+             stream)
+
+
+class Q8Cache:
+    """A kvb_q8_cache over torch tensors of the current device, with the workspace for up
+    to ``max_queries`` rows per head.  Tensors not given are allocated; lengths, weights
+    and the status word then start at zero.  Calls on one cache share its workspace, so
+    order them on one stream.
+
+    Marshalling only: every method calls the C entry point named in its docstring."""
+
+    def __init__(self, heads: int, head_dim: int, capacity: int, block: int = 64, dtype: int = KVB_BF16,
+                 max_queries: int = 1, with_mass: bool = False, K=None, V=None, k_scale=None, v_scale=None, len=None,
+                 mass=None):
+        import torch
+
+        def own(x, shape, dt, make):
+            if x is None:
+                return make(shape, dtype=dt, device="cuda")
+            _whole(x, shape, dt, "kvb_q8_cache")
+            return x
+
+        if block not in (16, 32, 64, 128) or capacity % block:
+            raise KvbError(1, "kvb_q8_cache")
+        self.heads, self.head_dim, self.capacity, self.block = heads, head_dim, capacity, block
+        self.dtype, self.max_queries = dtype, max_queries
+        self.torch_dtype = torch.float32 if dtype == KVB_F32 else torch.bfloat16
+        self.K = own(K, (heads, capacity, head_dim), torch.uint8, torch.empty)
+        self.V = own(V, (heads, capacity, head_dim), torch.uint8, torch.empty)
+        self.k_scale = own(k_scale, (heads, capacity // block), torch.float32, torch.empty)
+        self.v_scale = own(v_scale, (heads, capacity // block), torch.float32, torch.empty)
+        self.len = own(len, (heads,), torch.int32, torch.zeros)
+        self.mass = own(mass, (heads, capacity), torch.float32, torch.zeros) if mass is not None or with_mass else None
+        self.status_word = torch.zeros(1, dtype=torch.int32, device="cuda")
+        self.c = kvb_q8_cache(heads, head_dim, capacity, block, self.K.data_ptr(), self.V.data_ptr(),
+                              self.k_scale.data_ptr(), self.v_scale.data_ptr(), self.len.data_ptr(), _ptr(self.mass),
+                              self.status_word.data_ptr())
+        self.nbytes = kvb_q8_workspace_size(self.c, max_queries, dtype)
+        if self.nbytes == 0:
+            raise KvbError(1, "kvb_q8_workspace_size")
+        self._buf = torch.empty(self.nbytes + 256, dtype=torch.uint8, device="cuda")
+        self.ws = (self._buf.data_ptr() + 255) & ~255
+
+    def append(self, K, V, start=None, stream=None) -> None:
+        """kvb_q8_append: K, V [heads][n][d] in any row order; start int32 [heads] or None."""
+        import torch
+        shape = (self.heads, K.shape[1] if K.dim() == 3 else -1, self.head_dim)
+        ks = _rows(K, shape, self.dtype, "kvb_q8_append")
+        vs = _rows(V, shape, self.dtype, "kvb_q8_append")
+        _whole(start, (self.heads,), torch.int32, "kvb_q8_append")
+        kvb_q8_append(self.c, K, ks[0], ks[1], V, vs[0], vs[1], shape[1], self.dtype, start, stream)
+
+    def _queries(self, Q, lse, where: str) -> int:
+        import torch
+        n = Q.shape[1] if Q.dim() == 3 else 0
+        _whole(Q, (self.heads, n, self.head_dim), self.torch_dtype, where)
+        _whole(lse, (self.heads, n), torch.float32, where)
+        return n
+
+    def attend(self, Q, O, lse=None, scale: float = 0.0, stream=None) -> None:
+        """kvb_q8_attend: Q, O [heads][Nq][d], lse f32 [heads][Nq] or None."""
+        n = self._queries(Q, lse, "kvb_q8_attend")
+        _whole(O, Q.shape, self.torch_dtype, "kvb_q8_attend")
+        kvb_q8_attend(self.c, Q, n, self.dtype, scale, O, lse, self.ws, self.nbytes, stream)
+
+    def accumulate(self, Q, lse, decay: float = 1.0, prev=None, scale: float = 0.0, stream=None) -> None:
+        """kvb_q8_mass: ``mass`` = decay * prev + the weights of these queries; prev None is
+        the present ``mass``."""
+        import torch
+        n = self._queries(Q, lse, "kvb_q8_mass")
+        _whole(prev, (self.heads, self.capacity), torch.float32, "kvb_q8_mass")
+        kvb_q8_mass(self.c, Q, n, self.dtype, scale, lse, decay, self.mass if prev is None else prev, self.ws,
+                    self.nbytes, stream)
+
+    def evict(self, to: "Q8Cache", budget: int, sink: int = 0, recent: int = 0, kept=None, stream=None) -> None:
+        """kvb_q8_evict into another cache; kept int32 [heads][budget] or None."""
+        import torch
+        _whole(kept, (self.heads, budget), torch.int32, "kvb_q8_evict")
+        kvb_q8_evict(self.c, to.c, budget, sink, recent, kept, self.ws, self.nbytes, stream)
+
+    def status(self) -> int:
+        """The status word (synchronises)."""
+        return int(self.status_word.item())
 
 
 class Bank:
