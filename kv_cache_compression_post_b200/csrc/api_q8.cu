@@ -33,13 +33,16 @@ Q8View view(const kvb_q8_cache* c) {
 
 bool dtype_ok(kvb_dtype t) { return t == KVB_BF16 || t == KVB_F32; }
 
-// One scratch serves every call on a cache: attention partials, or the positions an
-// eviction keeps.
+// One scratch serves every call on a cache: partials of the row-tile kernels, the
+// positions an eviction keeps, or what a chunk of queries needs, each from its start.
 struct Scratch {
   float* part = nullptr;
   int* kept = nullptr;
+  Q8ChunkScratch chunk{};
   size_t bytes = 0;
 };
+
+bool chunk_kernel(int32_t rows, kvb_dtype dtype) { return dtype == KVB_BF16 && rows >= kQ8ChunkRows; }
 
 Scratch scratch(const kvb_q8_cache* c, int32_t max_queries, kvb_dtype dtype, void* ws) {
   Scratch s;
@@ -48,6 +51,16 @@ Scratch scratch(const kvb_q8_cache* c, int32_t max_queries, kvb_dtype dtype, voi
   Carver e(ws);
   s.kept = e.take<int>(static_cast<size_t>(c->heads) * c->capacity);
   s.bytes = a.bytes() > e.bytes() ? a.bytes() : e.bytes();
+  if (chunk_kernel(max_queries, dtype)) {
+    const size_t rows = static_cast<size_t>(c->heads) * max_queries;
+    Carver q(ws);
+    s.chunk.hi = q.take<uint8_t>(rows * c->head_dim);
+    s.chunk.lo = q.take<uint8_t>(rows * c->head_dim);
+    s.chunk.coef = q.take<float>(rows);
+    s.chunk.part = q.take<float>(q8_chunk_part_floats(c->head_dim));
+    s.chunk.cnt = q.take<unsigned int>(static_cast<size_t>(c->heads) * ((max_queries + 255) / 256) * 2);
+    if (q.bytes() > s.bytes) s.bytes = q.bytes();
+  }
   return s;
 }
 
@@ -118,6 +131,7 @@ kvb_status kvb_q8_attend(const kvb_q8_cache* c, const void* Q, int32_t Nq, kvb_d
   a.part = s.part;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == KVB_F32) return cuda_status(launch_q8_attend_f32(a, dev.n_sm, st));
+  if (chunk_kernel(Nq, dtype)) return cuda_status(launch_q8_attend_chunk(a, s.chunk, dev.n_sm, st));
   return cuda_status(launch_q8_attend_rows(a, dev.n_sm, st));
 }
 

@@ -27,6 +27,10 @@ bool make_tmap_bf16(CUtensorMap* m, const void* base, int d, long long rows, int
 // Tensor map over the augmented rows [heads][rows][32] bf16 (64 bytes per row),
 // box 16 x box_rows x 1, 32-byte swizzle (one K=16 slice of an MMA operand).
 bool make_tmap_aug(CUtensorMap* m, const void* base, long long rows, int heads, int box_rows);
+// Tensor map over bytes [heads][rows][d] (d 64 or 128), box d x box_rows x 1, zero fill
+// out of bounds; swizzled over the d bytes of a row (the K-major operand of an 8-bit
+// MMA), or as the rows lie.
+bool make_tmap_u8(CUtensorMap* m, const void* base, int d, long long rows, int heads, int box_rows, bool swizzled);
 
 // Every kernel launch of the library goes through one of these, constructed just
 // before the launch in the same scope: it counts the launch and, while tracing is

@@ -225,6 +225,25 @@ cudaError_t launch_q8_mass_f32(const Q8MassArgs& a, int n_sm, cudaStream_t st);
 // their maxima and sums
 inline size_t q8_part_floats(int d) { return static_cast<size_t>(kQ8MaxCtas) * 2 * (16 * d + 32); }
 
+// Scratch of the tensor-core kernels for chunks of queries: the queries' E4M3 parts and
+// row coefficients, and for attention the partials of cut units (two slots of two
+// 128-row tiles per CTA) with their arrival counters.
+struct Q8ChunkScratch {
+  uint8_t* hi;           // [H][Nq][d]
+  uint8_t* lo;
+  float* coef;           // [H][Nq]
+  float* part;           // q8_chunk_part_floats(d)
+  unsigned int* cnt;     // [H][pairs of query tiles][2]
+};
+inline size_t q8_chunk_part_floats(int d) { return static_cast<size_t>(4) * kQ8MaxCtas * (128 * d + 256); }
+cudaError_t launch_q8_split_q(const void* Q, long long rows, int d, float scale, const Q8ChunkScratch& s, int ncnt,
+                              int n_sm, cudaStream_t st);
+cudaError_t launch_q8_attend_chunk(const Q8AttendArgs& a, const Q8ChunkScratch& s, int n_sm, cudaStream_t st);
+
+// Rows per head from which a bf16 call takes the tensor-core chunk kernel instead of
+// the 16-row tiles.
+constexpr int kQ8ChunkRows = 17;
+
 struct Q8EvictArgs {
   Q8View src;
   const float* mass;

@@ -1,0 +1,643 @@
+// Attention over the 8-bit cache for chunks of queries, on the 5th-generation tensor
+// cores.
+//
+// The codes are multiplied as they lie.  A bf16 query element has 8 significant bits
+// and E4M3 holds 4, so with the row scaled by a power of two to a largest element in
+// [2^7, 2^8) every element is the exact sum of two E4M3 parts, q = hi + lo, down to
+// 2^-17 of the row's largest:
+//     S = hi K^T + lo K^T        2 x kind::f8f6f4, K the cache's bytes from TMA
+// which costs the tensor time of one bf16 product and never widens K.
+// P V cannot be split so cheaply (every weight would be rounded twice, by the warps
+// that are the scarce resource), so V is widened: a warpgroup of its own turns each V
+// tile into fp16 (exact, two codes per instruction) in the layout the MMA reads, and
+// clears rows behind the head's length, where anything may lie.  fp16 rather than bf16
+// also makes P eight times more exact than a bf16 kernel's.
+// Scales: K's block scale multiplies a 16-token chunk's scores inside the FFMA that
+// feeds the exponential; V's rides in the exponent, P' = 2^(x + log2 vs - m + kPBias)
+// with m the running maximum of x + log2 vs, and the row sum adds P' / vs per chunk.
+// Neither costs an instruction per score.
+//
+// Work: units of (head, pair of 128-query tiles A, B), split over a persistent grid at
+// 128-token tiles (Q8Split); a unit cut between CTAs is finished by whichever of its
+// pieces comes last, so no CTA waits for another.  TMEM: S_A, S_B, O_A, O_B (128
+// columns each), P_t over S_t's first half.  The MMA warp issues PV_A(j-1), S_A(j),
+// PV_B(j-1), S_B(j): one tile's softmax runs under the other's products.
+// Warps: 0 Q and K loads, 1 MMA, 2 TMEM, 3 V loads, 4-7 V widening, 8-11 softmax of
+// tile A, 12-15 of tile B (one thread per row).
+#include "host_util.h"
+#include "q8.cuh"
+#include "sm100.cuh"
+
+namespace kvb {
+using namespace sm100;
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kTile = 128;  // queries per query tile, tokens per key tile
+constexpr int kBarBytes = 256;
+constexpr int kKStages = 3, kV8Stages = 2, kVStages = 2;
+constexpr float kRescale = 8.f;   // the running maximum moves when it grows by more (log2)
+constexpr float kPBias = 6.f;     // P' <= 2^(kRescale + kPBias) < 65504
+// cost of a key tile to a pair of query tiles, to a lone one; least share of a CTA
+constexpr int kW2 = 8, kW1 = 7, kMinCost = 8 * kW2;
+// registers per thread of each warpgroup: loads and MMA, widening, softmax (x2).  Their
+// sum must not pass the launch's (checked on the host against the compiled kernel).
+constexpr int kRegsControl = 56, kRegsWiden = 80, kRegsSoftmax = 184;
+
+__device__ __forceinline__ uint32_t kbytes(int d) { return static_cast<uint32_t>(kTile) * d; }
+
+struct alignas(8) Bars {
+  uint64_t q_full, q_empty;
+  uint64_t k_full[kKStages], k_empty[kKStages];
+  uint64_t v8_full[kV8Stages], v8_empty[kV8Stages], v_full[kVStages], v_empty[kVStages];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t mma_done;
+  uint64_t grp[2];
+  uint32_t tmem_base;
+  int abort;
+  int last[2];
+};
+static_assert(sizeof(Bars) <= kBarBytes, "barrier block overflows its reservation");
+
+struct Maps {
+  CUtensorMap hi, lo, k, v;
+};
+
+struct Args {
+  Q8AttendArgs a;
+  const float* coef;   // [H][Nq]: raw score -> log2 units (but for the token's scale)
+  unsigned int* cnt;   // [H][npair][2] arrivals, zeroed by the split kernel
+};
+
+// D[tmem] (+)= A[smem] * B[smem]^T, kind::f8f6f4 (E4M3 here), 32 channels per instruction
+__device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// --------------------------------------------------------------- query parts
+// One warp per row: hi, lo codes and the row's coefficient.  Also zeroes the arrival
+// counters of the launch that follows.
+template <int D>
+__global__ void __launch_bounds__(256) q8_split_q_kernel(const __nv_bfloat16* Q, long long rows, float scale,
+                                                         uint8_t* hi, uint8_t* lo, float* coef, unsigned int* cnt,
+                                                         int ncnt) {
+  pdl_wait();
+  pdl_trigger();
+  const long long gt = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const long long nt = static_cast<long long>(gridDim.x) * blockDim.x;
+  for (long long i = gt; i < ncnt; i += nt) cnt[i] = 0u;
+  const int lane = threadIdx.x & 31;
+  constexpr int kE = D / 32;  // elements per lane: 4 or 2
+  for (long long row = gt >> 5; row < rows; row += nt >> 5) {
+    float f[kE];
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(Q + row * D) + lane * (kE / 2);
+#pragma unroll
+    for (int k = 0; k < kE / 2; ++k) {
+      const float2 x = unpack_bf16x2(__ldg(p + k));
+      f[2 * k] = x.x;
+      f[2 * k + 1] = x.y;
+    }
+    float mx = 0.f;
+#pragma unroll
+    for (int k = 0; k < kE; ++k)
+      if (fabsf(f[k]) <= 3.4e38f) mx = fmaxf(mx, fabsf(f[k]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const int e = max(exponent_of(mx), -100) - 7;  // mx 2^-e in [2^7, 2^8)
+    const float down = pow2f(-e);
+    uint32_t h = 0u, l = 0u;
+#pragma unroll
+    for (int k = 0; k < kE; k += 2) {
+      // an infinite element becomes a NaN: its row is NaN, as its scores would be
+      const float x = fabsf(f[k]) <= 3.4e38f ? f[k] * down : NAN, y = fabsf(f[k + 1]) <= 3.4e38f ? f[k + 1] * down : NAN;
+      const uint32_t c = f32x2_to_e4m3x2(x, y);
+      const float2 b = e4m3x2_to_f32x2(c);
+      h |= c << (8 * k);
+      l |= f32x2_to_e4m3x2(x - b.x, y - b.y) << (8 * k);
+    }
+    if constexpr (D == 128) {
+      reinterpret_cast<uint32_t*>(hi + row * D)[lane] = h;
+      reinterpret_cast<uint32_t*>(lo + row * D)[lane] = l;
+    } else {
+      reinterpret_cast<uint16_t*>(hi + row * D)[lane] = static_cast<uint16_t>(h);
+      reinterpret_cast<uint16_t*>(lo + row * D)[lane] = static_cast<uint16_t>(l);
+    }
+    if (lane == 0) coef[row] = pow2f(e) * scale * kLog2e;
+  }
+}
+
+// ----------------------------------------------------------------- attention
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const __grid_constant__ Maps maps, const Args args) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Q8Sched sch;
+  __shared__ Q8Walk s_it[8];
+  __shared__ Q8Piece s_pc[8];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const Q8AttendArgs& a = args.a;
+  constexpr uint32_t kCodeTile = kTile * D, kHalfTile = kTile * D * 2;  // bytes of a code tile, of an fp16 one
+  uint8_t* sQ = smem;                          // hi, lo of A; hi, lo of B
+  uint8_t* sK = sQ + 4 * kCodeTile;
+  uint8_t* sV8 = sK + kKStages * kCodeTile;
+  uint8_t* sV = sV8 + kV8Stages * kCodeTile;
+  Bars* bars = reinterpret_cast<Bars*>(sV + kVStages * kHalfTile);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int npair = (a.Nq + 2 * kTile - 1) / (2 * kTile);
+  const bool single = ((a.Nq + kTile - 1) / kTile) & 1;  // the last pair is a lone tile
+
+  if (tid == 0) {
+    mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_empty, 1);
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(&bars->k_full[i], 1);
+      mbar_init(&bars->k_empty[i], 1);
+    }
+    for (int i = 0; i < kV8Stages; ++i) {
+      mbar_init(&bars->v8_full[i], 1);
+      mbar_init(&bars->v8_empty[i], 4);
+    }
+    for (int i = 0; i < kVStages; ++i) {
+      mbar_init(&bars->v_full[i], 4);
+      mbar_init(&bars->v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->s_full[i], 1);
+      mbar_init(&bars->p_full[i], 4);
+      mbar_init(&bars->o_full[i], 1);
+      mbar_init(&bars->grp[i], 4);
+    }
+    mbar_init(&bars->mma_done, 1);
+    bars->abort = 0;
+    fence_barrier_init();
+  }
+  // lengths, query parts and coefficients come from earlier work on the stream
+  pdl_wait();
+  pdl_trigger();
+  q8_build_sched(&sch, a.c.len, a.c.cap, a.c.H, npair, kTile, kW2, single ? kW1 : kW2, gridDim.x, kMinCost);
+  if (static_cast<int>(blockIdx.x) >= sch.G) return;  // no share of the work
+  if (warp == 2) {
+    tmem_alloc(&bars->tmem_base, 512);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  volatile int* abort = &bars->abort;
+  Q8Split S{&sch, a.c.H, npair, kW2, single ? kW1 : kW2};
+  int* status = a.c.status;
+  auto ntq = [&](int p) { return (single && p == npair - 1) ? 1 : 2; };
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
+    if (warp == 0 && lane == 0) {
+      // ------------------------------------------------------------ Q and K loads
+      prefetch_tmap(&maps.hi);
+      prefetch_tmap(&maps.lo);
+      prefetch_tmap(&maps.k);
+      bool ok = true;
+      int g = 0, np = 0;
+      Q8Walk it;
+      it.init(S, blockIdx.x);
+      Q8Piece pc;
+      while (ok && it.next(S, pc)) {
+        for (int j = pc.j0; j < pc.j1; ++j) {
+          const int st = g % kKStages;
+          if (!(ok = mbar_wait(&bars->k_empty[st], ((g / kKStages) & 1) ^ 1, abort, status))) break;
+          mbar_arrive_expect_tx(&bars->k_full[st], kCodeTile);
+          tma_load_3d(sK + st * kCodeTile, &maps.k, &bars->k_full[st], 0, j * kTile, pc.h);
+          ++g;
+          if (j == pc.j0) {
+            // this piece's queries, once the previous piece's S products are done
+            if (np > 0 && !(ok = mbar_wait(&bars->q_empty, (np - 1) & 1, abort, status))) break;
+            const int nt = ntq(pc.r);
+            mbar_arrive_expect_tx(&bars->q_full, nt * 2 * kCodeTile);
+            for (int t = 0; t < nt; ++t) {
+              const int y = (pc.r * 2 + t) * kTile;
+              tma_load_3d(sQ + (2 * t) * kCodeTile, &maps.hi, &bars->q_full, 0, y, pc.h);
+              tma_load_3d(sQ + (2 * t + 1) * kCodeTile, &maps.lo, &bars->q_full, 0, y, pc.h);
+            }
+            ++np;
+          }
+        }
+      }
+      if (!ok) {
+        // let loads in flight land before the CTA exits
+        if (np > 0) mbar_wait_drain(&bars->q_full, (np - 1) & 1, 200000000ull);
+        for (int i = max(0, g - kKStages); i < g; ++i)
+          mbar_wait_drain(&bars->k_full[i % kKStages], (i / kKStages) & 1, 200000000ull);
+      }
+    } else if (warp == 3 && lane == 0) {
+      // ------------------------------------------------------------ V loads
+      prefetch_tmap(&maps.v);
+      bool ok = true;
+      int g = 0;
+      Q8Walk it;
+      it.init(S, blockIdx.x);
+      Q8Piece pc;
+      while (ok && it.next(S, pc)) {
+        for (int j = pc.j0; j < pc.j1; ++j) {
+          const int st = g % kV8Stages;
+          if (!(ok = mbar_wait(&bars->v8_empty[st], ((g / kV8Stages) & 1) ^ 1, abort, status))) break;
+          mbar_arrive_expect_tx(&bars->v8_full[st], kCodeTile);
+          tma_load_3d(sV8 + st * kCodeTile, &maps.v, &bars->v8_full[st], 0, j * kTile, pc.h);
+          ++g;
+        }
+      }
+      if (!ok)
+        for (int i = max(0, g - kV8Stages); i < g; ++i)
+          mbar_wait_drain(&bars->v8_full[i % kV8Stages], (i / kV8Stages) & 1, 200000000ull);
+    } else if (warp == 1 && lane == 0) {
+      // ------------------------------------------------------------ MMA
+      // f32 accumulator (bit 4), formats 0: E4M3 for kind::f8f6f4, fp16 for kind::f16
+      const uint32_t idS = (1u << 4) | (static_cast<uint32_t>(kTile >> 3) << 17) | (8u << 24);
+      const uint32_t idO = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) | (8u << 24);
+      const uint32_t qB = smem_u32(sQ), kB = smem_u32(sK), vB = smem_u32(sV);
+      constexpr uint32_t kLayout = D == 128 ? 2u : 4u;  // 128- or 64-byte swizzle: a row of codes
+      bool ok = true, issued = false;
+      int g = 0, np = 0;
+      int ns[2] = {0, 0};
+      Q8Walk it;
+      it.init(S, blockIdx.x);
+      Q8Piece pc;
+      auto pv = [&](int t, int vst, bool first) {
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          mma_f16_ts(tmem + 256 + t * kTile, tmem + t * kTile + kk * 8,
+                     sdesc_sw128(vB + vst * kHalfTile + kk * 2048, 16384, 1024), idO, (!first || kk > 0) ? 1u : 0u);
+      };
+      while (ok && it.next(S, pc)) {
+        if (!(ok = mbar_wait(&bars->q_full, np & 1, abort, status))) break;
+        tc_fence_after();
+        const int nt = ntq(pc.r);
+        for (int j = pc.j0; j < pc.j1 && ok; ++j) {
+          const int kst = g % kKStages;
+          const int vprev = (g + kVStages - 1) % kVStages;
+          if (!(ok = mbar_wait(&bars->k_full[kst], (g / kKStages) & 1, abort, status))) break;
+          if (j > pc.j0 && !(ok = mbar_wait(&bars->v_full[vprev], ((g - 1) / kVStages) & 1, abort, status))) break;
+          tc_fence_after();
+          for (int t = 0; t < nt; ++t) {
+            if (j > pc.j0) {
+              if (!(ok = mbar_wait(&bars->p_full[t], (ns[t] - 1) & 1, abort, status))) break;
+              tc_fence_after();
+              pv(t, vprev, j - 1 == pc.j0);
+            }
+            for (int part = 0; part < 2; ++part)
+              for (int kk = 0; kk < D / 32; ++kk)
+                mma_f8_ss(tmem + t * kTile, sdesc(qB + (2 * t + part) * kCodeTile + kk * 32, 16, 8 * D, kLayout),
+                          sdesc(kB + kst * kCodeTile + kk * 32, 16, 8 * D, kLayout), idS, (part > 0 || kk > 0) ? 1u : 0u);
+            issued = true;
+            mma_commit(&bars->s_full[t]);
+            ++ns[t];
+          }
+          if (!ok) break;
+          mma_commit(&bars->k_empty[kst]);
+          if (j > pc.j0) mma_commit(&bars->v_empty[vprev]);
+          if (j == pc.j1 - 1) mma_commit(&bars->q_empty);
+          ++g;
+        }
+        if (!ok) break;
+        const int vst = (g - 1) % kVStages;
+        if (!(ok = mbar_wait(&bars->v_full[vst], ((g - 1) / kVStages) & 1, abort, status))) break;
+        for (int t = 0; t < nt && ok; ++t) {
+          if (!(ok = mbar_wait(&bars->p_full[t], (ns[t] - 1) & 1, abort, status))) break;
+          tc_fence_after();
+          pv(t, vst, pc.j1 - 1 == pc.j0);
+          mma_commit(&bars->o_full[t]);
+        }
+        if (!ok) break;
+        mma_commit(&bars->v_empty[vst]);
+        ++np;
+      }
+      if (!ok && issued) {
+        // no MMA may still write TMEM when it is freed
+        mma_commit(&bars->mma_done);
+        mbar_wait_drain(&bars->mma_done, 0, 200000000ull);
+      }
+    }
+  } else if (warp < 8) {
+    // -------------------------------------------------------------- V widening
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWiden));
+    const int wt = tid - 128;
+    bool ok = true;
+    int g = 0;
+    Q8Walk it;
+    it.init(S, blockIdx.x);
+    Q8Piece pc;
+    while (ok && it.next(S, pc)) {
+      const int n = q8_len(a.c.len, pc.h, a.c.cap);
+      for (int j = pc.j0; j < pc.j1; ++j, ++g) {
+        const int s8 = g % kV8Stages, st = g % kVStages;
+        ok = mbar_wait(&bars->v8_full[s8], (g / kV8Stages) & 1, abort, status) &&
+             mbar_wait(&bars->v_empty[st], ((g / kVStages) & 1) ^ 1, abort, status);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        const int nv = min(kTile, n - j * kTile);
+        const uint8_t* src = sV8 + s8 * kCodeTile;
+        uint8_t* dst = sV + st * kHalfTile;
+#pragma unroll 8
+        for (int i = 0; i < D / 8; ++i) {
+          const int u = (wt + i * 128) % (D / 8), row = (wt + i * 128) / (D / 8);
+          const uint2 c = *reinterpret_cast<const uint2*>(src + row * D + u * 8);
+          uint4 w = make_uint4(0u, 0u, 0u, 0u);
+          if (row < nv)
+            w = make_uint4(e4m3x2_to_f16x2(c.x), e4m3x2_to_f16x2(c.x >> 16), e4m3x2_to_f16x2(c.y),
+                           e4m3x2_to_f16x2(c.y >> 16));
+          *reinterpret_cast<uint4*>(dst + (u >> 3) * 16384 + row * 128 + (((u & 7) ^ (row & 7)) << 4)) = w;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bars->v_full[st]);
+          mbar_arrive(&bars->v8_empty[s8]);
+        }
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int t = (warp - 8) >> 2;
+    const int q = warp & 3;       // TMEM lane quarter
+    const int r = q * 32 + lane;  // row of the query tile
+    const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
+    const uint32_t tS = tmem + t * kTile + lane_off;
+    const uint32_t tO = tmem + 256 + t * kTile + lane_off;
+    const int blocks = a.c.cap / a.c.block;
+    constexpr size_t kSlot = static_cast<size_t>(kTile) * D + 2 * kTile;
+    constexpr size_t kMl = static_cast<size_t>(kTile) * D;  // m, then l, behind O in a slot
+    bool ok = true;
+    int ns = 0, npt = 0, ngs = 0;
+    auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
+    };
+    auto group_sync = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->grp[t]);
+      return wait_warp(&bars->grp[t], (ngs++) & 1);
+    };
+    Q8Walk& it = s_it[warp - 8];
+    Q8Piece& pc = s_pc[warp - 8];
+    if (lane == 0) it.init(S, blockIdx.x);
+    __syncwarp();
+    for (;;) {
+      int more = 0;
+      __syncwarp();
+      if (lane == 0) more = it.next(S, pc) ? 1 : 0;
+      more = __shfl_sync(0xffffffffu, more, 0);
+      __syncwarp();
+      if (!more || !ok) break;
+      if (t >= ntq(pc.r)) continue;
+      const int n = q8_len(a.c.len, pc.h, a.c.cap);
+      const int qrow = (pc.r * 2 + t) * kTile + r;
+      const size_t row = static_cast<size_t>(pc.h) * a.Nq + qrow;
+      const float coef = qrow < a.Nq ? __ldg(args.coef + row) : 1.f;
+      const float* ks = a.c.ks + static_cast<size_t>(pc.h) * blocks;
+      const float* vs = a.c.vs + static_cast<size_t>(pc.h) * blocks;
+      // lane i holds the scales of a tile's chunk i (16 tokens), fetched a tile ahead
+      auto block_of = [&](int j) { return min(j * kTile + (lane & 7) * 16, n - 1) / a.c.block; };
+      float nk = __ldg(ks + block_of(pc.j0)), nv_s = __ldg(vs + block_of(pc.j0));
+      float m = -INFINITY, l = 0.f;
+      for (int j = pc.j0; j < pc.j1; ++j) {
+        const float kc = nk, vc = nv_s;
+        if (j + 1 < pc.j1) {
+          nk = __ldg(ks + block_of(j + 1));
+          nv_s = __ldg(vs + block_of(j + 1));
+        }
+        const float lvc = lg2_approx(vc), ivc = 1.f / vc;
+        const int nv = n - j * kTile;
+        if (!(ok = wait_warp(&bars->s_full[t], ns & 1))) break;
+        ++ns;
+        tc_fence_after();
+        uint32_t v0[32], v1[32], v2[32], v3[32];
+        tmem_ld32(tS + 0, v0);
+        tmem_ld32(tS + 32, v1);
+        tmem_ld32(tS + 64, v2);
+        tmem_ld32(tS + 96, v3);
+        tmem_wait_ld_reg(v0);
+        tmem_wait_ld_reg(v1);
+        tmem_wait_ld_reg(v2);
+        tmem_wait_ld_reg(v3);
+        auto X = [&](int k) -> uint32_t& {
+          return k < 32 ? v0[k] : (k < 64 ? v1[k - 32] : (k < 96 ? v2[k - 64] : v3[k - 96]));
+        };
+        auto F = [&](int k) { return __uint_as_float(X(k)); };
+        if (nv < kTile) {
+#pragma unroll
+          for (int k = 0; k < kTile; ++k)
+            if (k >= nv) X(k) = __float_as_uint(-INFINITY);
+        }
+        // row maximum in log2 units: a chunk's raw maximum, scaled
+        float mt = -INFINITY;
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch) {
+          const int k = ch * 16;
+          const float c0 = fmax3(F(k), F(k + 1), F(k + 2)), c1 = fmax3(F(k + 3), F(k + 4), F(k + 5)),
+                      c2 = fmax3(F(k + 6), F(k + 7), F(k + 8)), c3 = fmax3(F(k + 9), F(k + 10), F(k + 11)),
+                      c4 = fmax3(F(k + 12), F(k + 13), F(k + 14));
+          const float c = fmax3(fmax3(c0, c1, c2), fmax3(c3, c4, F(k + 15)), c0);
+          const float av = fmaxf(__shfl_sync(0xffffffffu, kc, ch) * coef, 1.2e-38f);
+          mt = fmaxf(mt, fmaf(c, av, __shfl_sync(0xffffffffu, lvc, ch)));
+        }
+        float alpha = 1.f;
+        bool resc = false;
+        if (j == pc.j0) {
+          m = mt;
+        } else if (mt > m + kRescale) {
+          alpha = ex2_approx(m - mt);
+          m = mt;
+          resc = true;
+        }
+        float rs = 0.f;
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch) {
+          const float av = fmaxf(__shfl_sync(0xffffffffu, kc, ch) * coef, 1.2e-38f);
+          const float b = __shfl_sync(0xffffffffu, lvc, ch) + (kPBias - m);
+          float ra = 0.f, rb = 0.f;
+          uint32_t pk[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int k = ch * 16 + 2 * i;
+            const float px = ex2_approx(fmaf(F(k), av, b));
+            const float py = ex2_approx(fmaf(F(k + 1), av, b));
+            ra += px;
+            rb += py;
+            pk[i] = pack_f16x2(px, py);
+          }
+          tmem_st8(tS + ch * 8, pk);
+          rs = fmaf(ra + rb, __shfl_sync(0xffffffffu, ivc, ch), rs);
+        }
+        // rare: the maximum moved.  O_t is stable here (PV_t(j-1) completed before S_t(j)
+        // did) and PV_t(j) waits for this tile's P.
+        if (__any_sync(0xffffffffu, resc)) {
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t v[32];
+            tmem_ld32(tO + c * 32, v);
+            tmem_wait_ld_reg(v);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha);
+            tmem_st32(tO + c * 32, v);
+          }
+        }
+        l = fmaf(l, alpha, rs);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_full[t]);
+      }
+      if (!ok) break;
+      if (!(ok = wait_warp(&bars->o_full[t], npt & 1))) break;
+      ++npt;
+      tc_fence_after();
+      __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.O) + row * D;
+      if (pc.npieces == 1) {
+        const float inv = 1.f / l;
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t v[32];
+          tmem_ld32(tO + c * 32, v);
+          tmem_wait_ld_reg(v);
+          if (qrow < a.Nq) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+              uint4 o;
+              o.x = pack_bf16x2(__uint_as_float(v[k + 0]) * inv, __uint_as_float(v[k + 1]) * inv);
+              o.y = pack_bf16x2(__uint_as_float(v[k + 2]) * inv, __uint_as_float(v[k + 3]) * inv);
+              o.z = pack_bf16x2(__uint_as_float(v[k + 4]) * inv, __uint_as_float(v[k + 5]) * inv);
+              o.w = pack_bf16x2(__uint_as_float(v[k + 6]) * inv, __uint_as_float(v[k + 7]) * inv);
+              *reinterpret_cast<uint4*>(orow + c * 32 + k) = o;
+            }
+          }
+        }
+        if (a.lse && qrow < a.Nq) a.lse[row] = (m - kPBias + log2f(l)) * kLn2;
+        continue;
+      }
+      // a piece of a cut unit: O as [D/4][128] float4, so that neighbouring rows are
+      // neighbouring words, then m and l
+      float* slot = a.part + static_cast<size_t>((blockIdx.x * 2 + pc.which) * 2 + t) * kSlot;
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t v[32];
+        tmem_ld32(tO + c * 32, v);
+        tmem_wait_ld_reg(v);
+#pragma unroll
+        for (int k = 0; k < 32; k += 4)
+          reinterpret_cast<float4*>(slot)[static_cast<size_t>(c * 8 + k / 4) * kTile + r] =
+              make_float4(__uint_as_float(v[k]), __uint_as_float(v[k + 1]), __uint_as_float(v[k + 2]),
+                          __uint_as_float(v[k + 3]));
+      }
+      slot[kMl + r] = m;
+      slot[kMl + kTile + r] = l;
+      __threadfence();
+      if (!(ok = group_sync())) break;
+      if (r == 0) {
+        unsigned int* cp = args.cnt + (static_cast<size_t>(pc.h) * npair + pc.r) * 2 + t;
+        bars->last[t] = atomicAdd(cp, 1u) + 1u == static_cast<unsigned int>(pc.npieces) ? 1 : 0;
+      }
+      if (!(ok = group_sync())) break;
+      if (!bars->last[t]) continue;
+      __threadfence();
+      // the last piece merges them all, row by row, in their order
+      auto slot_of = [&](int k) -> const float* {
+        return a.part + static_cast<size_t>(((pc.cfirst + k) * 2 + (k == 0 ? pc.wfirst : 0)) * 2 + t) * kSlot;
+      };
+      float M = -INFINITY;
+      for (int k = 0; k < pc.npieces; ++k) M = fmaxf(M, __ldcg(slot_of(k) + kMl + r));
+      float L = 0.f;
+      for (int k = 0; k < pc.npieces; ++k)
+        L += __ldcg(slot_of(k) + kMl + kTile + r) * ex2_approx(__ldcg(slot_of(k) + kMl + r) - M);
+      const float inv = 1.f / L;
+      for (int c4 = 0; c4 < D / 4; c4 += 2) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+        for (int k = 0; k < pc.npieces; ++k) {
+          const float* sk = slot_of(k);
+          const float w = ex2_approx(__ldcg(sk + kMl + r) - M) * inv;
+          const float4 u = __ldcg(reinterpret_cast<const float4*>(sk) + static_cast<size_t>(c4) * kTile + r);
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(sk) + static_cast<size_t>(c4 + 1) * kTile + r);
+          x.x = fmaf(w, u.x, x.x), x.y = fmaf(w, u.y, x.y), x.z = fmaf(w, u.z, x.z), x.w = fmaf(w, u.w, x.w);
+          y.x = fmaf(w, v.x, y.x), y.y = fmaf(w, v.y, y.y), y.z = fmaf(w, v.z, y.z), y.w = fmaf(w, v.w, y.w);
+        }
+        if (qrow < a.Nq)
+          *reinterpret_cast<uint4*>(orow + c4 * 4) =
+              make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+      }
+      if (a.lse && qrow < a.Nq) a.lse[row] = (M - kPBias + log2f(L)) * kLn2;
+    }
+    // rows of heads without tokens: zeros (lse -inf), spread over the CTAs
+    if (ok) {
+      for (int h = 0; h < a.c.H; ++h) {
+        if (sch.T[h] != 0) continue;
+        for (int p = 0; p < npair; ++p) {
+          if ((h * npair + p) % sch.G != static_cast<int>(blockIdx.x) || t >= ntq(p)) continue;
+          const int qrow = (p * 2 + t) * kTile + r;
+          if (qrow >= a.Nq) continue;
+          const size_t row = static_cast<size_t>(h) * a.Nq + qrow;
+          uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.O) + row * D);
+          for (int c = 0; c < D / 8; ++c) o[c] = make_uint4(0u, 0u, 0u, 0u);
+          if (a.lse) a.lse[row] = -INFINITY;
+        }
+      }
+    }
+  }
+
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+size_t smem_bytes() {
+  return 1024 + static_cast<size_t>(kTile) * D * (4 + kKStages + kV8Stages + 2 * kVStages) + kBarBytes;
+}
+
+template <int D>
+cudaError_t launch(const Q8AttendArgs& a, const Q8ChunkScratch& s, int n_sm, cudaStream_t st) {
+  const int npair = (a.Nq + 2 * kTile - 1) / (2 * kTile);
+  const long long rows = static_cast<long long>(a.c.H) * a.Nq;
+  Maps maps;
+  if (!make_tmap_u8(&maps.hi, s.hi, D, a.Nq, a.c.H, kTile, true) ||
+      !make_tmap_u8(&maps.lo, s.lo, D, a.Nq, a.c.H, kTile, true) ||
+      !make_tmap_u8(&maps.k, a.c.K, D, a.c.cap, a.c.H, kTile, true) ||
+      !make_tmap_u8(&maps.v, a.c.V, D, a.c.cap, a.c.H, kTile, false))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(q8_attend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem_bytes<D>()));
+  if (e != cudaSuccess) return e;
+  // the warpgroups' register shares come out of what the launch is given: more would
+  // wait for ever
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, q8_attend_kernel<D>);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs * 4 < kRegsControl + kRegsWiden + 2 * kRegsSoftmax) return cudaErrorLaunchOutOfResources;
+  e = launch_q8_split_q(a.Q, rows, D, a.scale, s, a.c.H * npair * 2, n_sm, st);
+  if (e != cudaSuccess) return e;
+  Args args{a, s.coef, s.cnt};
+  args.a.part = s.part;
+  LaunchTrace trace("q8_attend_kernel", st);
+  return launch_pdl(q8_attend_kernel<D>, dim3(n_sm < kQ8MaxCtas ? n_sm : kQ8MaxCtas), dim3(kThreads), smem_bytes<D>(),
+                    st, maps, args);
+}
+
+}  // namespace
+
+cudaError_t launch_q8_split_q(const void* Q, long long rows, int d, float scale, const Q8ChunkScratch& s, int ncnt,
+                              int n_sm, cudaStream_t st) {
+  const long long need = (rows + 7) / 8;
+  const int grid = static_cast<int>(need < 16LL * n_sm ? need : 16LL * n_sm);
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(Q);
+  LaunchTrace trace("q8_split_q_kernel", st);
+  return d == 128 ? launch_pdl(q8_split_q_kernel<128>, dim3(grid), dim3(256), 0, st, q, rows, scale, s.hi, s.lo, s.coef,
+                               s.cnt, ncnt)
+                  : launch_pdl(q8_split_q_kernel<64>, dim3(grid), dim3(256), 0, st, q, rows, scale, s.hi, s.lo, s.coef,
+                               s.cnt, ncnt);
+}
+
+cudaError_t launch_q8_attend_chunk(const Q8AttendArgs& a, const Q8ChunkScratch& s, int n_sm, cudaStream_t st) {
+  return a.c.d == 128 ? launch<128>(a, s, n_sm, st) : launch<64>(a, s, n_sm, st);
+}
+
+}  // namespace kvb
