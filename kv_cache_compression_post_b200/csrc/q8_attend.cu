@@ -19,11 +19,22 @@
 //
 // Work: units of (head, pair of 128-query tiles A, B), split over a persistent grid at
 // 128-token tiles (Q8Split); a unit cut between CTAs is finished by whichever of its
-// pieces comes last, so no CTA waits for another.  TMEM: S_A, S_B, O_A, O_B (128
-// columns each), P_t over S_t's first half.  The MMA warp issues PV_A(j-1), S_A(j),
-// PV_B(j-1), S_B(j): one tile's softmax runs under the other's products.
-// Warps: 0 Q and K loads, 1 MMA, 2 TMEM, 3 V loads, 4-7 V widening, 8-11 softmax of
-// tile A, 12-15 of tile B (one thread per row).
+// pieces comes last, so no CTA waits for another.
+// TMEM: S_A, S_B, O_A, O_B (128 columns each), P_t over S_t's first half.  Per key tile
+// and query tile: S_t, softmax, P_t V, and S_t of the next tile behind it.
+// What bounds it.  A 256 x 128 step has 2048 clk of tensor time and 2048 clk of
+// exponentials per SM and takes ~4400 (at 1.8 GHz, the power cap active): softmax and
+// products of one query tile follow one another, so the two tiles have to alternate.
+// Kept for that, each measured on 12 heads x 4680 queries x 15600 tokens: one MMA warp
+// per query tile, operands in uniform registers (627 -> 557 us with the scales' ring;
+// issuing from one divergent lane cost ~110 clk an MMA), and turns at the exponentials
+// (552 -> 507 us; left alone the tiles fall into step and wait together).  Not kept: a
+// part of the exponentials as polynomials on the FMA pipe (+6 % for one pair in eight:
+// issue, not the exponential unit, is short in a turn); 64-token steps with two score
+// buffers (542 us: N = 64 products read the query rows twice as often); two warpgroups
+// per query tile, by steps (554 us) or by columns (584 us).
+// Warps: 0 loads, 1 and 3 MMAs of tile A and B, 2 TMEM and scales, 4-7 V widening,
+// 8-11 softmax of tile A, 12-15 of tile B (one thread per row).
 #include "host_util.h"
 #include "q8.cuh"
 #include "sm100.cuh"
@@ -35,24 +46,25 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kTile = 128;  // queries per query tile, tokens per key tile
-constexpr int kBarBytes = 256;
-constexpr int kKStages = 3, kV8Stages = 2, kVStages = 2;
+constexpr int kBarBytes = 512;
+constexpr int kKStages = 3, kV8Stages = 2, kVStages = 2, kScStages = 4;
 constexpr float kRescale = 8.f;   // the running maximum moves when it grows by more (log2)
 constexpr float kPBias = 6.f;     // P' <= 2^(kRescale + kPBias) < 65504
 // cost of a key tile to a pair of query tiles, to a lone one; least share of a CTA
 constexpr int kW2 = 8, kW1 = 7, kMinCost = 8 * kW2;
 // registers per thread of each warpgroup: loads and MMA, widening, softmax (x2).  Their
 // sum must not pass the launch's (checked on the host against the compiled kernel).
-constexpr int kRegsControl = 56, kRegsWiden = 80, kRegsSoftmax = 184;
-
-__device__ __forceinline__ uint32_t kbytes(int d) { return static_cast<uint32_t>(kTile) * d; }
+constexpr int kRegsControl = 64, kRegsWiden = 80, kRegsSoftmax = 184;
 
 struct alignas(8) Bars {
   uint64_t q_full, q_empty;
   uint64_t k_full[kKStages], k_empty[kKStages];
   uint64_t v8_full[kV8Stages], v8_empty[kV8Stages], v_full[kVStages], v_empty[kVStages];
-  uint64_t s_full[2], p_full[2], o_full[2];
-  uint64_t mma_done;
+  uint64_t s_full[2], p_full[2];
+  uint64_t o_full[2];
+  uint64_t sc_full[2][kScStages], sc_empty[kScStages];  // a tile's scales, per query tile that reads them
+  uint64_t mma_done[2];
+  uint64_t turn[2][4];  // the exponentials of a tile pair take turns: per query tile just done, lane quarter
   uint64_t grp[2];
   uint32_t tmem_base;
   int abort;
@@ -140,6 +152,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const __grid_con
   __shared__ Q8Sched sch;
   __shared__ Q8Walk s_it[8];
   __shared__ Q8Piece s_pc[8];
+  // per ring slot: K scales, log2 of V's and their reciprocals, of eight 16-token chunks
+  __shared__ alignas(16) float sScale[kScStages * 24];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const Q8AttendArgs& a = args.a;
   constexpr uint32_t kCodeTile = kTile * D, kHalfTile = kTile * D * 2;  // bytes of a code tile, of an fp16 one
@@ -155,10 +169,10 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const __grid_con
 
   if (tid == 0) {
     mbar_init(&bars->q_full, 1);
-    mbar_init(&bars->q_empty, 1);
+    mbar_init(&bars->q_empty, 2);  // the rings are handed back by both query tiles' MMA warps
     for (int i = 0; i < kKStages; ++i) {
       mbar_init(&bars->k_full[i], 1);
-      mbar_init(&bars->k_empty[i], 1);
+      mbar_init(&bars->k_empty[i], 2);
     }
     for (int i = 0; i < kV8Stages; ++i) {
       mbar_init(&bars->v8_full[i], 1);
@@ -166,15 +180,21 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const __grid_con
     }
     for (int i = 0; i < kVStages; ++i) {
       mbar_init(&bars->v_full[i], 4);
-      mbar_init(&bars->v_empty[i], 1);
+      mbar_init(&bars->v_empty[i], 2);
+    }
+    for (int i = 0; i < kScStages; ++i) {
+      mbar_init(&bars->sc_full[0][i], 1);
+      mbar_init(&bars->sc_full[1][i], 1);
+      mbar_init(&bars->sc_empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->s_full[i], 1);
       mbar_init(&bars->p_full[i], 4);
       mbar_init(&bars->o_full[i], 1);
       mbar_init(&bars->grp[i], 4);
+      for (int k = 0; k < 4; ++k) mbar_init(&bars->turn[i][k], 1);
+      mbar_init(&bars->mma_done[i], 1);
     }
-    mbar_init(&bars->mma_done, 1);
     bars->abort = 0;
     fence_barrier_init();
   }
@@ -198,25 +218,25 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const __grid_con
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
     if (warp == 0 && lane == 0) {
-      // ------------------------------------------------------------ Q and K loads
+      // ------------------------------------------------------------ loads
       prefetch_tmap(&maps.hi);
       prefetch_tmap(&maps.lo);
       prefetch_tmap(&maps.k);
+      prefetch_tmap(&maps.v);
       bool ok = true;
       int g = 0, np = 0;
       Q8Walk it;
       it.init(S, blockIdx.x);
       Q8Piece pc;
       while (ok && it.next(S, pc)) {
-        for (int j = pc.j0; j < pc.j1; ++j) {
-          const int st = g % kKStages;
-          if (!(ok = mbar_wait(&bars->k_empty[st], ((g / kKStages) & 1) ^ 1, abort, status))) break;
+        for (int j = pc.j0; j < pc.j1; ++j, ++g) {
+          const int st = g % kKStages, s8 = g % kV8Stages;
+          if (!(ok = mbar_wait_step(&bars->k_empty[st], ((g / kKStages) & 1) ^ 1, abort, status))) break;
           mbar_arrive_expect_tx(&bars->k_full[st], kCodeTile);
           tma_load_3d(sK + st * kCodeTile, &maps.k, &bars->k_full[st], 0, j * kTile, pc.h);
-          ++g;
           if (j == pc.j0) {
             // this piece's queries, once the previous piece's S products are done
-            if (np > 0 && !(ok = mbar_wait(&bars->q_empty, (np - 1) & 1, abort, status))) break;
+            if (np > 0 && !(ok = mbar_wait_step(&bars->q_empty, (np - 1) & 1, abort, status))) break;
             const int nt = ntq(pc.r);
             mbar_arrive_expect_tx(&bars->q_full, nt * 2 * kCodeTile);
             for (int t = 0; t < nt; ++t) {
@@ -226,105 +246,152 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const __grid_con
             }
             ++np;
           }
+          if (!(ok = mbar_wait_step(&bars->v8_empty[s8], ((g / kV8Stages) & 1) ^ 1, abort, status))) break;
+          mbar_arrive_expect_tx(&bars->v8_full[s8], kCodeTile);
+          tma_load_3d(sV8 + s8 * kCodeTile, &maps.v, &bars->v8_full[s8], 0, j * kTile, pc.h);
         }
       }
       if (!ok) {
-        // let loads in flight land before the CTA exits
-        if (np > 0) mbar_wait_drain(&bars->q_full, (np - 1) & 1, 200000000ull);
-        for (int i = max(0, g - kKStages); i < g; ++i)
-          mbar_wait_drain(&bars->k_full[i % kKStages], (i / kKStages) & 1, 200000000ull);
+        // let loads in flight land before the CTA exits (barriers a load was not issued on
+        // complete their older phases at once, or run into the short limit)
+        if (np > 0) mbar_wait_drain(&bars->q_full, (np - 1) & 1, 20000000ull);
+        for (int i = max(0, g - kKStages); i <= g; ++i) {
+          mbar_wait_drain(&bars->k_full[i % kKStages], (i / kKStages) & 1, 20000000ull);
+          if (i > g - kV8Stages) mbar_wait_drain(&bars->v8_full[i % kV8Stages], (i / kV8Stages) & 1, 20000000ull);
+        }
       }
-    } else if (warp == 3 && lane == 0) {
-      // ------------------------------------------------------------ V loads
-      prefetch_tmap(&maps.v);
+    } else if (warp == 2) {
+      // ------------------------------------------------------------ scales
+      // lanes 0..15: K's, then V's scale of a tile's eight 16-token chunks, fetched a tile
+      // ahead of the ring
+      const int blocks = a.c.cap / a.c.block;
       bool ok = true;
-      int g = 0;
+      int g = 0, gb = 0;  // tiles so far; those that query tile B reads too
       Q8Walk it;
       it.init(S, blockIdx.x);
       Q8Piece pc;
       while (ok && it.next(S, pc)) {
-        for (int j = pc.j0; j < pc.j1; ++j) {
-          const int st = g % kV8Stages;
-          if (!(ok = mbar_wait(&bars->v8_empty[st], ((g / kV8Stages) & 1) ^ 1, abort, status))) break;
-          mbar_arrive_expect_tx(&bars->v8_full[st], kCodeTile);
-          tma_load_3d(sV8 + st * kCodeTile, &maps.v, &bars->v8_full[st], 0, j * kTile, pc.h);
-          ++g;
+        const int n = q8_len(a.c.len, pc.h, a.c.cap);
+        const bool pair = ntq(pc.r) == 2;
+        const float* sp = (lane < 8 ? a.c.ks : a.c.vs) + static_cast<size_t>(pc.h) * blocks;
+        auto fetch = [&](int j) {
+          return lane < 16 ? __ldg(sp + min(j * kTile + (lane & 7) * 16, n - 1) / a.c.block) : 1.f;
+        };
+        float next = fetch(pc.j0);
+        for (int j = pc.j0; j < pc.j1; ++j, ++g) {
+          const float s = next;
+          if (j + 1 < pc.j1) next = fetch(j + 1);
+          const int st = g % kScStages;
+          ok = mbar_wait_step(&bars->sc_empty[st], ((g / kScStages) & 1) ^ 1, abort, status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          float* to = sScale + st * 24 + (lane & 7);
+          if (lane < 8) {
+            to[0] = s;
+          } else if (lane < 16) {
+            to[8] = lg2_approx(s);
+            to[16] = 1.f / s;
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&bars->sc_full[0][st]);
+            if (pair) mbar_arrive(&bars->sc_full[1][gb % kScStages]);
+          }
+          if (pair) ++gb;
         }
       }
-      if (!ok)
-        for (int i = max(0, g - kV8Stages); i < g; ++i)
-          mbar_wait_drain(&bars->v8_full[i % kV8Stages], (i / kV8Stages) & 1, 200000000ull);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1 || warp == 3) {
       // ------------------------------------------------------------ MMA
+      // One warp per query tile: the issuing thread is held until the tensor core has taken
+      // its MMAs, and then needs ~400 clk for the barriers of its next ones; with two, the
+      // other tile's MMAs run meanwhile.  One elected lane issues.
+      const int t = warp >> 1;
+      const bool leader = elect_one();
       // f32 accumulator (bit 4), formats 0: E4M3 for kind::f8f6f4, fp16 for kind::f16
-      const uint32_t idS = (1u << 4) | (static_cast<uint32_t>(kTile >> 3) << 17) | (8u << 24);
-      const uint32_t idO = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) | (8u << 24);
-      const uint32_t qB = smem_u32(sQ), kB = smem_u32(sK), vB = smem_u32(sV);
+      constexpr uint32_t idS = (1u << 4) | (static_cast<uint32_t>(kTile >> 3) << 17) | (8u << 24);
+      constexpr uint32_t idO = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) | (8u << 24);
       constexpr uint32_t kLayout = D == 128 ? 2u : 4u;  // 128- or 64-byte swizzle: a row of codes
+      const uint64_t qd = sdesc(smem_u32(sQ) + 2 * t * kCodeTile, 16, 8 * D, kLayout);
+      const uint64_t kd = sdesc(smem_u32(sK), 16, 8 * D, kLayout);
+      const uint64_t vd = sdesc_sw128(smem_u32(sV), 16384, 1024);
+      const uint32_t dS = tmem + t * kTile, dO = tmem + 256 + t * kTile;
       bool ok = true, issued = false;
-      int g = 0, np = 0;
-      int ns[2] = {0, 0};
+      int kst = 0, vst = 0, sst = 0, np = 0;  // ring positions of the next K, V, scale slot
+      uint32_t kph = 0, vph = 0, pph = 0;     // phases of k_full, v_full, p_full[t]
       Q8Walk it;
       it.init(S, blockIdx.x);
       Q8Piece pc;
-      auto pv = [&](int t, int vst, bool first) {
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          mma_f16_ts(tmem + 256 + t * kTile, tmem + t * kTile + kk * 8,
-                     sdesc_sw128(vB + vst * kHalfTile + kk * 2048, 16384, 1024), idO, (!first || kk > 0) ? 1u : 0u);
+      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait_step(bar, parity, abort, status));
       };
-      while (ok && it.next(S, pc)) {
-        if (!(ok = mbar_wait(&bars->q_full, np & 1, abort, status))) break;
-        tc_fence_after();
-        const int nt = ntq(pc.r);
-        for (int j = pc.j0; j < pc.j1 && ok; ++j) {
-          const int kst = g % kKStages;
-          const int vprev = (g + kVStages - 1) % kVStages;
-          if (!(ok = mbar_wait(&bars->k_full[kst], (g / kKStages) & 1, abort, status))) break;
-          if (j > pc.j0 && !(ok = mbar_wait(&bars->v_full[vprev], ((g - 1) / kVStages) & 1, abort, status))) break;
+      for (;;) {
+        if (!__all_sync(0xffffffffu, it.next(S, pc))) break;
+        const int nj = __reduce_min_sync(0xffffffffu, pc.j1 - pc.j0);
+        const bool mine = t < ntq(pc.r);  // else this tile has no rows: only hand the slots back
+        if (!(ok = wait(&bars->q_full, np & 1))) break;
+        for (int j = 0; j <= nj && ok; ++j) {
+          // P V of tile j - 1, then the scores of tile j, over the P that has just been read
+          if (j < nj && !(ok = wait(&bars->k_full[kst], kph))) break;
+          if (j > 0 && !(ok = wait(&bars->v_full[vst], vph))) break;
           tc_fence_after();
-          for (int t = 0; t < nt; ++t) {
-            if (j > pc.j0) {
-              if (!(ok = mbar_wait(&bars->p_full[t], (ns[t] - 1) & 1, abort, status))) break;
+          if (mine) {
+            if (j > 0) {
+              if (!(ok = wait(&bars->p_full[t], pph))) break;
+              pph ^= 1u;
               tc_fence_after();
-              pv(t, vprev, j - 1 == pc.j0);
+              if (leader) {
+                const uint64_t vb = vd + static_cast<uint32_t>(vst) * (kHalfTile >> 4);
+#pragma unroll
+                for (int kk = 0; kk < kTile / 16; ++kk)
+                  mma_f16_ts(dO, dS + kk * 8, vb + kk * 128, idO, (j > 1 || kk > 0) ? 1u : 0u);
+                if (j == nj) mma_commit(&bars->o_full[t]);
+              }
             }
-            for (int part = 0; part < 2; ++part)
-              for (int kk = 0; kk < D / 32; ++kk)
-                mma_f8_ss(tmem + t * kTile, sdesc(qB + (2 * t + part) * kCodeTile + kk * 32, 16, 8 * D, kLayout),
-                          sdesc(kB + kst * kCodeTile + kk * 32, 16, 8 * D, kLayout), idS, (part > 0 || kk > 0) ? 1u : 0u);
+            if (j < nj && leader) {
+              const uint64_t kb = kd + static_cast<uint32_t>(kst) * (kCodeTile >> 4);
+#pragma unroll
+              for (int part = 0; part < 2; ++part)
+#pragma unroll
+                for (int kk = 0; kk < D / 32; ++kk)
+                  mma_f8_ss(dS, qd + part * (kCodeTile >> 4) + kk * 2, kb + kk * 2, idS, (part > 0 || kk > 0) ? 1u : 0u);
+              mma_commit(&bars->s_full[t]);
+            }
             issued = true;
-            mma_commit(&bars->s_full[t]);
-            ++ns[t];
           }
-          if (!ok) break;
-          mma_commit(&bars->k_empty[kst]);
-          if (j > pc.j0) mma_commit(&bars->v_empty[vprev]);
-          if (j == pc.j1 - 1) mma_commit(&bars->q_empty);
-          ++g;
+          if (j > 0) {
+            // P V done: V's slot is free, and so are the scales its softmax read
+            if (leader) {
+              mma_commit(&bars->v_empty[vst]);
+              mma_commit(&bars->sc_empty[sst]);
+            }
+            sst = (sst + 1) % kScStages;
+            if (++vst == kVStages) vst = 0, vph ^= 1u;
+          }
+          if (j < nj) {
+            if (leader) {
+              mma_commit(&bars->k_empty[kst]);
+              if (j == nj - 1) mma_commit(&bars->q_empty);
+            }
+            if (++kst == kKStages) kst = 0, kph ^= 1u;
+          }
         }
         if (!ok) break;
-        const int vst = (g - 1) % kVStages;
-        if (!(ok = mbar_wait(&bars->v_full[vst], ((g - 1) / kVStages) & 1, abort, status))) break;
-        for (int t = 0; t < nt && ok; ++t) {
-          if (!(ok = mbar_wait(&bars->p_full[t], (ns[t] - 1) & 1, abort, status))) break;
-          tc_fence_after();
-          pv(t, vst, pc.j1 - 1 == pc.j0);
-          mma_commit(&bars->o_full[t]);
-        }
-        if (!ok) break;
-        mma_commit(&bars->v_empty[vst]);
         ++np;
       }
       if (!ok && issued) {
         // no MMA may still write TMEM when it is freed
-        mma_commit(&bars->mma_done);
-        mbar_wait_drain(&bars->mma_done, 0, 200000000ull);
+        if (leader) mma_commit(&bars->mma_done[t]);
+        mbar_wait_drain(&bars->mma_done[t], 0, 200000000ull);
       }
     }
   } else if (warp < 8) {
     // -------------------------------------------------------------- V widening
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsWiden));
     const int wt = tid - 128;
+    constexpr int kUnits = D / 8;                  // 8-code units per row; a thread keeps its own
+    const int u = wt % kUnits, r0 = wt / kUnits;   // and takes every (128 / kUnits)-th row
+    constexpr int kStep = 128 / kUnits;            // 8 or 16 rows: the swizzle (row & 7) stays
+    const uint8_t* src0 = sV8 + wt * 8;
+    uint8_t* dst0 = sV + (u >> 3) * 16384 + r0 * 128 + (((u & 7) ^ (r0 & 7)) << 4);
     bool ok = true;
     int g = 0;
     Q8Walk it;
@@ -334,21 +401,25 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const __grid_con
       const int n = q8_len(a.c.len, pc.h, a.c.cap);
       for (int j = pc.j0; j < pc.j1; ++j, ++g) {
         const int s8 = g % kV8Stages, st = g % kVStages;
-        ok = mbar_wait(&bars->v8_full[s8], (g / kV8Stages) & 1, abort, status) &&
-             mbar_wait(&bars->v_empty[st], ((g / kVStages) & 1) ^ 1, abort, status);
+        ok = mbar_wait_step(&bars->v_empty[st], ((g / kVStages) & 1) ^ 1, abort, status);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        const int nv = min(kTile, n - j * kTile);
-        const uint8_t* src = sV8 + s8 * kCodeTile;
-        uint8_t* dst = sV + st * kHalfTile;
-#pragma unroll 8
-        for (int i = 0; i < D / 8; ++i) {
-          const int u = (wt + i * 128) % (D / 8), row = (wt + i * 128) / (D / 8);
-          const uint2 c = *reinterpret_cast<const uint2*>(src + row * D + u * 8);
-          uint4 w = make_uint4(0u, 0u, 0u, 0u);
-          if (row < nv)
-            w = make_uint4(e4m3x2_to_f16x2(c.x), e4m3x2_to_f16x2(c.x >> 16), e4m3x2_to_f16x2(c.y),
-                           e4m3x2_to_f16x2(c.y >> 16));
-          *reinterpret_cast<uint4*>(dst + (u >> 3) * 16384 + row * 128 + (((u & 7) ^ (row & 7)) << 4)) = w;
+        ok = mbar_wait_step(&bars->v8_full[s8], (g / kV8Stages) & 1, abort, status);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        const int nv = n - j * kTile - r0;
+        const uint8_t* src = src0 + s8 * kCodeTile;
+        uint8_t* dst = dst0 + st * kHalfTile;
+#pragma unroll
+        for (int b = 0; b < kUnits; b += 8) {
+          uint2 c[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) c[i] = *reinterpret_cast<const uint2*>(src + (b + i) * 1024);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if ((b + i) * kStep >= nv) c[i] = make_uint2(0u, 0u);
+            *reinterpret_cast<uint4*>(dst + (b + i) * kStep * 128) =
+                make_uint4(e4m3x2_to_f16x2(c[i].x), e4m3x2_to_f16x2(c[i].x >> 16), e4m3x2_to_f16x2(c[i].y),
+                           e4m3x2_to_f16x2(c[i].y >> 16));
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -367,13 +438,13 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const __grid_con
     const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
     const uint32_t tS = tmem + t * kTile + lane_off;
     const uint32_t tO = tmem + 256 + t * kTile + lane_off;
-    const int blocks = a.c.cap / a.c.block;
     constexpr size_t kSlot = static_cast<size_t>(kTile) * D + 2 * kTile;
     constexpr size_t kMl = static_cast<size_t>(kTile) * D;  // m, then l, behind O in a slot
     bool ok = true;
-    int ns = 0, npt = 0, ngs = 0;
+    // tiles of the CTA's walk so far, and those of them that this query tile takes part in
+    int ns = 0, npt = 0, ngs = 0, gt = 0, gm = 0, np2 = 0;
     auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
+      return __all_sync(0xffffffffu, mbar_wait_step(bar, parity, abort, status));
     };
     auto group_sync = [&]() -> bool {
       __syncwarp();
@@ -391,25 +462,20 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const __grid_con
       more = __shfl_sync(0xffffffffu, more, 0);
       __syncwarp();
       if (!more || !ok) break;
-      if (t >= ntq(pc.r)) continue;
+      if (t >= ntq(pc.r)) {
+        gt += pc.j1 - pc.j0;
+        continue;
+      }
       const int n = q8_len(a.c.len, pc.h, a.c.cap);
       const int qrow = (pc.r * 2 + t) * kTile + r;
       const size_t row = static_cast<size_t>(pc.h) * a.Nq + qrow;
+      const bool pair = ntq(pc.r) == 2;
       const float coef = qrow < a.Nq ? __ldg(args.coef + row) : 1.f;
-      const float* ks = a.c.ks + static_cast<size_t>(pc.h) * blocks;
-      const float* vs = a.c.vs + static_cast<size_t>(pc.h) * blocks;
-      // lane i holds the scales of a tile's chunk i (16 tokens), fetched a tile ahead
-      auto block_of = [&](int j) { return min(j * kTile + (lane & 7) * 16, n - 1) / a.c.block; };
-      float nk = __ldg(ks + block_of(pc.j0)), nv_s = __ldg(vs + block_of(pc.j0));
       float m = -INFINITY, l = 0.f;
-      for (int j = pc.j0; j < pc.j1; ++j) {
-        const float kc = nk, vc = nv_s;
-        if (j + 1 < pc.j1) {
-          nk = __ldg(ks + block_of(j + 1));
-          nv_s = __ldg(vs + block_of(j + 1));
-        }
-        const float lvc = lg2_approx(vc), ivc = 1.f / vc;
+      for (int j = pc.j0; j < pc.j1; ++j, ++gt, ++gm) {
         const int nv = n - j * kTile;
+        const float* sc = sScale + (gt % kScStages) * 24;
+        if (!(ok = wait_warp(&bars->sc_full[t][gm % kScStages], (gm / kScStages) & 1))) break;
         if (!(ok = wait_warp(&bars->s_full[t], ns & 1))) break;
         ++ns;
         tc_fence_after();
@@ -431,49 +497,64 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const __grid_con
           for (int k = 0; k < kTile; ++k)
             if (k >= nv) X(k) = __float_as_uint(-INFINITY);
         }
-        // row maximum in log2 units: a chunk's raw maximum, scaled
-        float mt = -INFINITY;
+        // row maximum in log2 units: a 16-token chunk's raw maximum, scaled
+        float av[8], lv[8], mc[8];
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(sc + i), y = *reinterpret_cast<const float4*>(sc + 8 + i);
+          // at least the smallest normal float: -inf times it stays -inf
+          av[i] = fmaxf(x.x * coef, 1.2e-38f), av[i + 1] = fmaxf(x.y * coef, 1.2e-38f);
+          av[i + 2] = fmaxf(x.z * coef, 1.2e-38f), av[i + 3] = fmaxf(x.w * coef, 1.2e-38f);
+          lv[i] = y.x, lv[i + 1] = y.y, lv[i + 2] = y.z, lv[i + 3] = y.w;
+        }
 #pragma unroll
         for (int ch = 0; ch < 8; ++ch) {
           const int k = ch * 16;
           const float c0 = fmax3(F(k), F(k + 1), F(k + 2)), c1 = fmax3(F(k + 3), F(k + 4), F(k + 5)),
                       c2 = fmax3(F(k + 6), F(k + 7), F(k + 8)), c3 = fmax3(F(k + 9), F(k + 10), F(k + 11)),
                       c4 = fmax3(F(k + 12), F(k + 13), F(k + 14));
-          const float c = fmax3(fmax3(c0, c1, c2), fmax3(c3, c4, F(k + 15)), c0);
-          const float av = fmaxf(__shfl_sync(0xffffffffu, kc, ch) * coef, 1.2e-38f);
-          mt = fmaxf(mt, fmaf(c, av, __shfl_sync(0xffffffffu, lvc, ch)));
+          mc[ch] = fmaf(fmax3(fmax3(c0, c1, c2), fmax3(c3, c4, F(k + 15)), c0), av[ch], lv[ch]);
         }
-        float alpha = 1.f;
-        bool resc = false;
+        const float mt = fmax3(fmax3(mc[0], mc[1], mc[2]), fmax3(mc[3], mc[4], mc[5]), fmaxf(mc[6], mc[7]));
+        float alpha = 1.f, rs = 0.f;
+        bool moved = false;
         if (j == pc.j0) {
           m = mt;
         } else if (mt > m + kRescale) {
           alpha = ex2_approx(m - mt);
           m = mt;
-          resc = true;
+          moved = true;
         }
-        float rs = 0.f;
+        // The two query tiles' warps of a scheduler take turns at the exponentials.  Left to
+        // themselves they fall into step, and the exponential unit idles while both wait for
+        // their products.
+        if (pair && (t == 1 || np2 > 0) && !(ok = wait_warp(&bars->turn[t ^ 1][q], (t == 1 ? np2 : np2 - 1) & 1))) break;
+        const float mb = kPBias - m;
 #pragma unroll
         for (int ch = 0; ch < 8; ++ch) {
-          const float av = fmaxf(__shfl_sync(0xffffffffu, kc, ch) * coef, 1.2e-38f);
-          const float b = __shfl_sync(0xffffffffu, lvc, ch) + (kPBias - m);
-          float ra = 0.f, rb = 0.f;
+          const float2 a2 = make_float2(av[ch], av[ch]), b2 = make_float2(lv[ch] + mb, lv[ch] + mb);
+          float2 sum = make_float2(0.f, 0.f);
           uint32_t pk[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int k = ch * 16 + 2 * i;
-            const float px = ex2_approx(fmaf(F(k), av, b));
-            const float py = ex2_approx(fmaf(F(k + 1), av, b));
-            ra += px;
-            rb += py;
-            pk[i] = pack_f16x2(px, py);
+          for (int e = 0; e < 8; ++e) {
+            const int k = ch * 16 + 2 * e;
+            const float2 x = __ffma2_rn(make_float2(F(k), F(k + 1)), a2, b2);
+            const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            sum = __fadd2_rn(sum, p);
+            pk[e] = pack_f16x2(p.x, p.y);
           }
           tmem_st8(tS + ch * 8, pk);
-          rs = fmaf(ra + rb, __shfl_sync(0xffffffffu, ivc, ch), rs);
+          rs = fmaf(sum.x + sum.y, sc[16 + ch], rs);
         }
-        // rare: the maximum moved.  O_t is stable here (PV_t(j-1) completed before S_t(j)
-        // did) and PV_t(j) waits for this tile's P.
-        if (__any_sync(0xffffffffu, resc)) {
+        if (pair) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->turn[t][q]);
+          ++np2;
+        }
+        // O_t is stable here (PV_t(j-1) completed before S_t(j) did), and PV_t(j) waits for
+        // this tile's P
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t v[32];
             tmem_ld32(tO + c * 32, v);
@@ -496,6 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const __grid_con
       __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.O) + row * D;
       if (pc.npieces == 1) {
         const float inv = 1.f / l;
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t v[32];
           tmem_ld32(tO + c * 32, v);
@@ -518,6 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const __grid_con
       // a piece of a cut unit: O as [D/4][128] float4, so that neighbouring rows are
       // neighbouring words, then m and l
       float* slot = a.part + static_cast<size_t>((blockIdx.x * 2 + pc.which) * 2 + t) * kSlot;
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t v[32];
         tmem_ld32(tO + c * 32, v);
@@ -549,6 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const __grid_con
       for (int k = 0; k < pc.npieces; ++k)
         L += __ldcg(slot_of(k) + kMl + kTile + r) * ex2_approx(__ldcg(slot_of(k) + kMl + r) - M);
       const float inv = 1.f / L;
+#pragma unroll 1
       for (int c4 = 0; c4 < D / 4; c4 += 2) {
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
         for (int k = 0; k < pc.npieces; ++k) {
