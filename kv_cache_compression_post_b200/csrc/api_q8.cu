@@ -58,7 +58,8 @@ Scratch scratch(const kvb_q8_cache* c, int32_t max_queries, kvb_dtype dtype, voi
     s.chunk.lo = q.take<uint8_t>(rows * c->head_dim);
     s.chunk.coef = q.take<float>(rows);
     s.chunk.part = q.take<float>(q8_chunk_part_floats(c->head_dim));
-    s.chunk.cnt = q.take<unsigned int>(static_cast<size_t>(c->heads) * ((max_queries + 255) / 256) * 2);
+    const size_t cut = static_cast<size_t>(c->heads) * ((max_queries + 255) / 256) * 2;
+    s.chunk.cnt = q.take<unsigned int>(cut > kQ8MassCounters ? cut : kQ8MassCounters);
     if (q.bytes() > s.bytes) s.bytes = q.bytes();
   }
   return s;
@@ -156,6 +157,7 @@ kvb_status kvb_q8_mass(const kvb_q8_cache* c, const void* Q, int32_t Nq, kvb_dty
   a.mass = c->mass;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == KVB_F32) return cuda_status(launch_q8_mass_f32(a, dev.n_sm, st));
+  if (chunk_kernel(Nq, dtype)) return cuda_status(launch_q8_mass_chunk(a, s.chunk, dev.n_sm, st));
   return cuda_status(launch_q8_mass_rows(a, dev.n_sm, st));
 }
 
