@@ -1,78 +1,113 @@
 // kvb_q8_evict: cut every head to a budget by accumulated attention weight.
 //
-// q8_select_kernel, one CTA per head: the weight of the last token to stay is found
-// digit by digit (8 bits of the order-preserving integer of a float, from the top: a
-// radix select, four passes over the head's weights, which stay in L2), then each warp
-// counts and writes the positions of its own run of tokens, so the list comes out in
-// order and of equal weights the lower positions stay.
+// q8_select_kernel, a cluster of eight CTAs per head: the weight of the last token to
+// stay is found digit by digit (8 bits of the order-preserving integer of a float, from
+// the top: a radix select, four passes over keys held in shared memory, the CTAs'
+// histograms added over distributed shared memory), then each warp counts and writes the
+// positions of its own run of tokens, so the list comes out in order and of equal weights
+// the lower positions stay.  Bound by latency: a head has one answer per pass to wait for
+// (one CTA per head took 150 us for 8 heads of 131072 tokens).
 // q8_gather_kernel, one CTA per (block of the result, head, K or V): reads and writes
 // each kept row once.  The result's block takes the largest scale among its tokens;
 // rows from blocks of smaller scale are rounded anew (exactly scaled where both are
 // powers of two), others are copied bit for bit.
+#include <cooperative_groups.h>
+
 #include "host_util.h"
 #include "q8.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace kvb {
 namespace {
 
+constexpr int kSelCtas = 8;  // a head's cluster
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kCopies = 8;   // histograms, so that equal digits of a warp meet less often
+constexpr int kCopies = 8;         // histograms, so that equal digits of a warp meet less often
+constexpr int kSelKeys = 16384;    // keys of a CTA that stay in shared memory between the passes
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
   return w != w ? 0u : float_key(w + 0.f);  // NaN least; -0 as 0
 }
 
-__global__ void __launch_bounds__(kSelThreads) q8_select_kernel(const Q8EvictArgs a) {
-  __shared__ int hist[kCopies][256];
-  __shared__ int s_sum[256];
-  __shared__ int s_above[kSelWarps], s_equal[kSelWarps];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_need;
+struct SelShared {
+  uint32_t key[kSelKeys];
+  int hist[kCopies][256];
+  int sum[2][256];     // this CTA's digit counts, by parity of the pass
+  int total[256];      // the head's
+  int above[kSelWarps], equal[kSelWarps];
+  int cta[2];          // this CTA's
+  uint32_t prefix;
+  int need;
+};
+
+__global__ void __cluster_dims__(kSelCtas, 1, 1) __launch_bounds__(kSelThreads) q8_select_kernel(const Q8EvictArgs a) {
+  extern __shared__ uint8_t smem[];
+  SelShared& s = *reinterpret_cast<SelShared*>(smem);
+  cg::cluster_group cluster = cg::this_cluster();
   pdl_wait();
   pdl_trigger();
-  const int h = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n = q8_len(a.src.len, h, a.src.cap);
   int* kept = a.kept + static_cast<size_t>(h) * a.budget;
   if (n <= a.budget) {
-    for (int i = tid; i < n; i += kSelThreads) kept[i] = i;
-    if (tid == 0) a.len[h] = n;
+    for (int i = rank * kSelThreads + tid; i < n; i += kSelCtas * kSelThreads) kept[i] = i;
+    if (rank == 0 && tid == 0) a.len[h] = n;
     return;
   }
   const float* mass = a.mass + static_cast<size_t>(h) * a.src.cap;
   const int lo = a.sink, hi = n - a.recent;
   const int need = a.budget - a.sink - a.recent;
-  // the need-th largest key of [lo, hi): prefix of the digits found so far, and how many
-  // of the keys that share it stay
+  // every warp of the cluster has one run of tokens, a multiple of 32 long
+  const int run = ((n + kSelCtas * kSelWarps - 1) / (kSelCtas * kSelWarps) + 31) & ~31;
+  const int c0 = min(rank * kSelWarps * run, n), c1 = min(c0 + kSelWarps * run, n);
+  const bool held = c1 - c0 <= kSelKeys;
+  auto key_at = [&](int i) { return held ? s.key[i - c0] : weight_key(__ldg(mass + i)); };
+  if (held) {
+    for (int i = c0 + tid; i < c1; i += kSelThreads) s.key[i - c0] = weight_key(__ldg(mass + i));
+  }
+  // the need-th largest key of [lo, hi): the digits found so far, and how many of the keys
+  // that share them all stay
   uint32_t thr = 0xFFFFFFFFu;
   int quota = 0;
   if (need > 0) {
     if (tid == 0) {
-      s_prefix = 0u;
-      s_need = need;
+      s.prefix = 0u;
+      s.need = need;
     }
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < kCopies * 256; i += kSelThreads) (&hist[0][0])[i] = 0;
+    const int p0 = max(c0, lo), p1 = min(c1, hi);
+    for (int pass = 0; pass < 4; ++pass) {
+      const int shift = 24 - 8 * pass;
+      for (int i = tid; i < kCopies * 256; i += kSelThreads) (&s.hist[0][0])[i] = 0;
       __syncthreads();
-      const uint32_t prefix = s_prefix;
-      const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-      for (int i = lo + tid; i < hi; i += kSelThreads) {
-        const uint32_t k = weight_key(__ldg(mass + i));
-        if ((k & mask) == prefix) atomicAdd(&hist[tid % kCopies][(k >> shift) & 255u], 1);
+      const uint32_t prefix = s.prefix;
+      const int want = s.need;
+      const uint32_t mask = pass == 0 ? 0u : 0xFFFFFFFFu << (shift + 8);
+      for (int i = p0 + tid; i < p1; i += kSelThreads) {
+        const uint32_t k = key_at(i);
+        if ((k & mask) == prefix) atomicAdd(&s.hist[tid % kCopies][(k >> shift) & 255u], 1);
       }
       __syncthreads();
       if (tid < 256) {
         int v = 0;
 #pragma unroll
-        for (int c = 0; c < kCopies; ++c) v += hist[c][tid];
-        s_sum[tid] = v;
+        for (int c = 0; c < kCopies; ++c) v += s.hist[c][tid];
+        s.sum[pass & 1][tid] = v;
+      }
+      cluster.sync();
+      if (tid < 256) {
+        int v = 0;
+#pragma unroll
+        for (int c = 0; c < kSelCtas; ++c) v += cluster.map_shared_rank(&s.sum[pass & 1][0], c)[tid];
+        s.total[tid] = v;
       }
       __syncthreads();
       if (warp == 0) {
         // keys of larger digits, eight digits a lane, from the top
         int v[8], mine = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) mine += v[k] = s_sum[255 - lane * 8 - k];
+        for (int k = 0; k < 8; ++k) mine += v[k] = s.total[255 - lane * 8 - k];
         int above = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -80,14 +115,12 @@ __global__ void __launch_bounds__(kSelThreads) q8_select_kernel(const Q8EvictArg
           if (lane >= o) above += y;
         }
         above -= mine;
-        const int want = s_need;
-        __syncwarp();
         if (above < want && above + mine >= want) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             if (above < want && above + v[k] >= want) {
-              s_prefix = prefix | (static_cast<uint32_t>(255 - lane * 8 - k) << shift);
-              s_need = want - above;
+              s.prefix = prefix | (static_cast<uint32_t>(255 - lane * 8 - k) << shift);
+              s.need = want - above;
             }
             above += v[k];
           }
@@ -95,16 +128,16 @@ __global__ void __launch_bounds__(kSelThreads) q8_select_kernel(const Q8EvictArg
       }
       __syncthreads();
     }
-    thr = s_prefix;
-    quota = s_need;
+    thr = s.prefix;
+    quota = s.need;
+  } else {
+    __syncthreads();  // the held keys
   }
-  // each warp takes one run of tokens, a multiple of 32 long
-  const int run = ((n + kSelWarps - 1) / kSelWarps + 31) & ~31;
-  const int r0 = min(warp * run, n), r1 = min(r0 + run, n);
+  const int r0 = min(c0 + warp * run, n), r1 = min(r0 + run, n);
   auto state = [&](int i, bool& stays, bool& equal) {
     const bool in = i < r1;
     const bool forced = in && (i < lo || i >= hi);
-    const uint32_t k = in && !forced ? weight_key(__ldg(mass + i)) : 0u;
+    const uint32_t k = in && !forced ? key_at(i) : 0u;
     stays = forced || (in && k > thr);
     equal = in && !forced && need > 0 && k == thr;
   };
@@ -116,14 +149,26 @@ __global__ void __launch_bounds__(kSelThreads) q8_select_kernel(const Q8EvictArg
     equal_n += __popc(__ballot_sync(0xffffffffu, eq));
   }
   if (lane == 0) {
-    s_above[warp] = above;
-    s_equal[warp] = equal_n;
+    s.above[warp] = above;
+    s.equal[warp] = equal_n;
   }
   __syncthreads();
+  if (tid < 2) {
+    const int* v = tid ? s.equal : s.above;
+    int x = 0;
+    for (int w = 0; w < kSelWarps; ++w) x += v[w];
+    s.cta[tid] = x;
+  }
+  cluster.sync();
   int at = 0, eq_before = 0;
+  for (int c = 0; c < rank; ++c) {
+    const int* v = cluster.map_shared_rank(&s.cta[0], c);
+    at += v[0];
+    eq_before += v[1];
+  }
   for (int w = 0; w < warp; ++w) {
-    at += s_above[w];
-    eq_before += s_equal[w];
+    at += s.above[w];
+    eq_before += s.equal[w];
   }
   at += min(eq_before, quota);
   const uint32_t below = (1u << lane) - 1u;
@@ -137,7 +182,8 @@ __global__ void __launch_bounds__(kSelThreads) q8_select_kernel(const Q8EvictArg
     at += __popc(km);
     eq_before += __popc(em);
   }
-  if (tid == 0) a.len[h] = a.budget;
+  if (rank == 0 && tid == 0) a.len[h] = a.budget;
+  cluster.sync();  // no CTA leaves while another reads its counts
 }
 
 constexpr int kGatherThreads = 256;
@@ -207,7 +253,9 @@ cudaError_t launch_q8_evict(const Q8EvictArgs& a, cudaStream_t st) {
   cudaError_t e;
   {
     LaunchTrace trace("q8_select_kernel", st);
-    e = launch_pdl(q8_select_kernel, dim3(a.src.H), dim3(kSelThreads), 0, st, a);
+    e = cudaFuncSetAttribute(q8_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(SelShared)));
+    if (e == cudaSuccess)
+      e = launch_pdl(q8_select_kernel, dim3(kSelCtas, a.src.H), dim3(kSelThreads), sizeof(SelShared), st, a);
   }
   if (e != cudaSuccess) return e;
   LaunchTrace trace("q8_gather_kernel", st);

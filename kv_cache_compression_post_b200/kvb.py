@@ -159,6 +159,8 @@ def _ptr(x) -> Optional[int]:
 def _stream(s) -> Optional[int]:
     if s is None:
         import torch
+        if torch.cuda.is_initialized():     # the current stream's handle, without a Stream object around it
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(s, int):
         return s
@@ -333,28 +335,32 @@ def kvb_q8_evict(src: kvb_q8_cache, dst: kvb_q8_cache, budget: int, sink: int, r
 
 def _tensor_dtype(x, where: str) -> int:
     import torch
-    if x.dtype == torch.bfloat16:
+    if x.dtype is torch.bfloat16:
         return KVB_BF16
-    if x.dtype == torch.float32:
+    if x.dtype is torch.float32:
         return KVB_F32
     raise KvbError(1, where)
 
 
-def _rows(x, shape, dtype: int, where: str):
-    """A [heads][n][d] tensor of a call, in any order of its rows: its head and token
-    strides, after checking its shape, its type and that a row is contiguous."""
-    if tuple(x.shape) != tuple(shape) or _tensor_dtype(x, where) != dtype or not x.is_cuda or \
-            (x.stride(2) != 1 and shape[2] != 1):
+def _rows(x, shape, dtype, where: str):
+    """The head and token strides of a [heads][n][d] device tensor of a call, in any order
+    of its rows: its shape and type are checked, and that a row is contiguous.  The stride
+    of a dimension of one row says nothing and counts as 0."""
+    if x.shape != shape or x.dtype is not dtype or not x.is_cuda:
         raise KvbError(1, where)
-    # the stride of a dimension of one row says nothing
-    return (x.stride(0) if shape[0] > 1 else 0), (x.stride(1) if shape[1] > 1 else 0)
+    h, n, e = x.stride()
+    if e != 1 and shape[2] != 1:
+        raise KvbError(1, where)
+    return (h if shape[0] > 1 else 0), (n if shape[1] > 1 else 0)
 
 
-def _whole(x, shape, dtype, where: str) -> None:
-    """A contiguous device tensor of a call (None passes)."""
-    if x is not None and (tuple(x.shape) != tuple(shape) or x.dtype != dtype or not x.is_cuda or
-                          not x.is_contiguous()):
+def _whole(x, shape, dtype, where: str) -> int:
+    """The address of a contiguous device tensor of a call, checked (None passes, as 0)."""
+    if x is None:
+        return 0
+    if x.shape != shape or x.dtype is not dtype or not x.is_cuda or not x.is_contiguous():
         raise KvbError(1, where)
+    return x.data_ptr()
 
 
 def rope(X, pos, out, axis_pairs, base: float = 10000.0, pairing: int = KVB_ROPE_INTERLEAVED, inverse: bool = False,
@@ -363,14 +369,16 @@ def rope(X, pos, out, axis_pairs, base: float = 10000.0, pairing: int = KVB_ROPE
     token-major tensor, say), both of one type; pos int32 [tokens][3]."""
     import torch
     dtype = _tensor_dtype(X, "kvb_rope")
-    if X.dim() != 3:
+    if X.dim() != 3 or len(axis_pairs) != 3:
         raise KvbError(1, "kvb_rope")
-    h, n, d = X.shape
-    xs = _rows(X, (h, n, d), dtype, "kvb_rope")
-    os_ = _rows(out, (h, n, d), dtype, "kvb_rope")
-    _whole(pos, (n, 3), torch.int32, "kvb_rope")
-    kvb_rope(X, pos, h, n, d, dtype, axis_pairs, base, pairing, 1 if inverse else 0, xs[0], xs[1], out, os_[0], os_[1],
-             stream)
+    shape = X.shape
+    xh, xt = _rows(X, shape, X.dtype, "kvb_rope")
+    oh, ot = _rows(out, shape, X.dtype, "kvb_rope")
+    st = lib.kvb_rope(X.data_ptr(), _whole(pos, (shape[1], 3), torch.int32, "kvb_rope"), shape[0], shape[1], shape[2],
+                      dtype, (_i32 * 3)(*axis_pairs), base, pairing, 1 if inverse else 0, xh, xt, out.data_ptr(), oh,
+                      ot, _stream(stream))
+    if st:
+        raise KvbError(st, "kvb_rope")
 
 
 class Q8Cache:
@@ -379,7 +387,8 @@ class Q8Cache:
     and the status word then start at zero.  Calls on one cache share its workspace, so
     order them on one stream.
 
-    Marshalling only: every method calls the C entry point named in its docstring."""
+    Marshalling only: every method calls the C entry point named in its docstring, on the
+    tensors' addresses after checking their shapes, types and layouts."""
 
     def __init__(self, heads: int, head_dim: int, capacity: int, block: int = 64, dtype: int = KVB_BF16,
                  max_queries: int = 1, with_mass: bool = False, K=None, V=None, k_scale=None, v_scale=None, len=None,
@@ -407,6 +416,7 @@ class Q8Cache:
         self.c = kvb_q8_cache(heads, head_dim, capacity, block, self.K.data_ptr(), self.V.data_ptr(),
                               self.k_scale.data_ptr(), self.v_scale.data_ptr(), self.len.data_ptr(), _ptr(self.mass),
                               self.status_word.data_ptr())
+        self._ref = ctypes.byref(self.c)
         self.nbytes = kvb_q8_workspace_size(self.c, max_queries, dtype)
         if self.nbytes == 0:
             raise KvbError(1, "kvb_q8_workspace_size")
@@ -417,38 +427,45 @@ class Q8Cache:
         """kvb_q8_append: K, V [heads][n][d] in any row order; start int32 [heads] or None."""
         import torch
         shape = (self.heads, K.shape[1] if K.dim() == 3 else -1, self.head_dim)
-        ks = _rows(K, shape, self.dtype, "kvb_q8_append")
-        vs = _rows(V, shape, self.dtype, "kvb_q8_append")
-        _whole(start, (self.heads,), torch.int32, "kvb_q8_append")
-        kvb_q8_append(self.c, K, ks[0], ks[1], V, vs[0], vs[1], shape[1], self.dtype, start, stream)
-
-    def _queries(self, Q, lse, where: str) -> int:
-        import torch
-        n = Q.shape[1] if Q.dim() == 3 else 0
-        _whole(Q, (self.heads, n, self.head_dim), self.torch_dtype, where)
-        _whole(lse, (self.heads, n), torch.float32, where)
-        return n
+        kh, kt = _rows(K, shape, self.torch_dtype, "kvb_q8_append")
+        vh, vt = _rows(V, shape, self.torch_dtype, "kvb_q8_append")
+        st = lib.kvb_q8_append(self._ref, K.data_ptr(), kh, kt, V.data_ptr(), vh, vt, shape[1], self.dtype,
+                               _whole(start, (self.heads,), torch.int32, "kvb_q8_append"), _stream(stream))
+        if st:
+            raise KvbError(st, "kvb_q8_append")
 
     def attend(self, Q, O, lse=None, scale: float = 0.0, stream=None) -> None:
         """kvb_q8_attend: Q, O [heads][Nq][d], lse f32 [heads][Nq] or None."""
-        n = self._queries(Q, lse, "kvb_q8_attend")
-        _whole(O, Q.shape, self.torch_dtype, "kvb_q8_attend")
-        kvb_q8_attend(self.c, Q, n, self.dtype, scale, O, lse, self.ws, self.nbytes, stream)
+        import torch
+        n = Q.shape[1] if Q.dim() == 3 else 0
+        shape = (self.heads, n, self.head_dim)
+        st = lib.kvb_q8_attend(self._ref, _whole(Q, shape, self.torch_dtype, "kvb_q8_attend"), n, self.dtype, scale,
+                               _whole(O, shape, self.torch_dtype, "kvb_q8_attend"),
+                               _whole(lse, (self.heads, n), torch.float32, "kvb_q8_attend"), self.ws, self.nbytes,
+                               _stream(stream))
+        if st:
+            raise KvbError(st, "kvb_q8_attend")
 
     def accumulate(self, Q, lse, decay: float = 1.0, prev=None, scale: float = 0.0, stream=None) -> None:
         """kvb_q8_mass: ``mass`` = decay * prev + the weights of these queries; prev None is
         the present ``mass``."""
         import torch
-        n = self._queries(Q, lse, "kvb_q8_mass")
-        _whole(prev, (self.heads, self.capacity), torch.float32, "kvb_q8_mass")
-        kvb_q8_mass(self.c, Q, n, self.dtype, scale, lse, decay, self.mass if prev is None else prev, self.ws,
-                    self.nbytes, stream)
+        n = Q.shape[1] if Q.dim() == 3 else 0
+        st = lib.kvb_q8_mass(self._ref, _whole(Q, (self.heads, n, self.head_dim), self.torch_dtype, "kvb_q8_mass"), n,
+                             self.dtype, scale, _whole(lse, (self.heads, n), torch.float32, "kvb_q8_mass"), decay,
+                             _whole(self.mass if prev is None else prev, (self.heads, self.capacity), torch.float32,
+                                    "kvb_q8_mass"), self.ws, self.nbytes, _stream(stream))
+        if st:
+            raise KvbError(st, "kvb_q8_mass")
 
     def evict(self, to: "Q8Cache", budget: int, sink: int = 0, recent: int = 0, kept=None, stream=None) -> None:
         """kvb_q8_evict into another cache; kept int32 [heads][budget] or None."""
         import torch
-        _whole(kept, (self.heads, budget), torch.int32, "kvb_q8_evict")
-        kvb_q8_evict(self.c, to.c, budget, sink, recent, kept, self.ws, self.nbytes, stream)
+        st = lib.kvb_q8_evict(self._ref, to._ref, budget, sink, recent,
+                              _whole(kept, (self.heads, budget), torch.int32, "kvb_q8_evict"), self.ws, self.nbytes,
+                              _stream(stream))
+        if st:
+            raise KvbError(st, "kvb_q8_evict")
 
     def status(self) -> int:
         """The status word (synchronises)."""
