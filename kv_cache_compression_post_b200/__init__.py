@@ -12,5 +12,6 @@ def __getattr__(name):
                                             "Q8Cache", "rope") \
             or name.startswith("KVB_"):
         from . import kvb as _kvb
-        return getattr(_kvb, name)
+        value = globals()[name] = getattr(_kvb, name)   # found here from now on
+        return value
     raise AttributeError(name)

@@ -28,7 +28,7 @@ kvb_status check_cache(const kvb_q8_cache* c) {
 }
 
 Q8View view(const kvb_q8_cache* c) {
-  return Q8View{c->heads, c->head_dim, c->capacity, c->block, c->K, c->V, c->k_scale, c->v_scale, c->len, c->status};
+  return Q8View{c->heads, c->head_dim, c->capacity, c->block, __builtin_ctz(c->block), c->K, c->V, c->k_scale, c->v_scale, c->len, c->status};
 }
 
 bool dtype_ok(kvb_dtype t) { return t == KVB_BF16 || t == KVB_F32; }

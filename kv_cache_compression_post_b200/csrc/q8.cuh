@@ -20,6 +20,7 @@ constexpr int kQ8MaxCtas = 160;  // grid cap of the kernels that split work (>= 
 
 struct Q8View {
   int H, d, cap, block;
+  int shift;  // block = 1 << shift
   const uint8_t* K;
   const uint8_t* V;
   const float* ks;

@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const __grid_con
       // ------------------------------------------------------------ scales
       // lanes 0..15: K's, then V's scale of a tile's eight 16-token chunks, fetched a tile
       // ahead of the ring
-      const int blocks = a.c.cap / a.c.block;
+      const int blocks = a.c.cap >> a.c.shift;
       bool ok = true;
       int g = 0, gb = 0;  // tiles so far; those that query tile B reads too
       Q8Walk it;
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const __grid_con
         const bool pair = ntq(pc.r) == 2;
         const float* sp = (lane < 8 ? a.c.ks : a.c.vs) + static_cast<size_t>(pc.h) * blocks;
         auto fetch = [&](int j) {
-          return lane < 16 ? __ldg(sp + min(j * kTile + (lane & 7) * 16, n - 1) / a.c.block) : 1.f;
+          return lane < 16 ? __ldg(sp + (min(j * kTile + (lane & 7) * 16, n - 1) >> a.c.shift)) : 1.f;
         };
         float next = fetch(pc.j0);
         for (int j = pc.j0; j < pc.j1; ++j, ++g) {

@@ -7,8 +7,8 @@
 // positions of its own run of tokens, so the list comes out in order and of equal weights
 // the lower positions stay.  Bound by latency: a head has one answer per pass to wait for
 // (one CTA per head took 150 us for 8 heads of 131072 tokens).
-// q8_gather_kernel, one CTA per (block of the result, head, K or V): reads and writes
-// each kept row once.  The result's block takes the largest scale among its tokens;
+// q8_gather_kernel, one CTA per 128 tokens of the result: reads and writes each kept row
+// once, every word of its rows in flight at once.  The result's block takes the largest scale among its tokens;
 // rows from blocks of smaller scale are rounded anew (exactly scaled where both are
 // powers of two), others are copied bit for bit.
 #include <cooperative_groups.h>
@@ -187,64 +187,68 @@ __global__ void __cluster_dims__(kSelCtas, 1, 1) __launch_bounds__(kSelThreads) 
 }
 
 constexpr int kGatherThreads = 256;
+constexpr int kGatherTok = 128;  // tokens of the result per CTA: one to eight blocks
 
-// sixteen codes times r, rounded to E4M3
+// four codes times r, rounded to E4M3
 __device__ __forceinline__ uint32_t rescale4(uint32_t c, float r) {
   const float2 x = e4m3x2_to_f32x2(c), y = e4m3x2_to_f32x2(c >> 16);
   return f32x2_to_e4m3x2(x.x * r, x.y * r) | (f32x2_to_e4m3x2(y.x * r, y.y * r) << 16);
 }
 
+template <int D>
 __global__ void __launch_bounds__(kGatherThreads) q8_gather_kernel(const Q8EvictArgs a) {
-  __shared__ int s_src[128];
-  __shared__ float s_ratio[128];
-  __shared__ float s_max[4];
+  __shared__ int s_src[kGatherTok];
+  __shared__ float s_scale[2][kGatherTok], s_to[2][kGatherTok / 16];
   pdl_wait();
   pdl_trigger();
-  const int b = blockIdx.x, h = blockIdx.y, kv = blockIdx.z, tid = threadIdx.x;
-  const int block = a.src.block, d = a.src.d;
+  const int t0 = blockIdx.x * kGatherTok, h = blockIdx.y, tid = threadIdx.x;
+  const int shift = a.src.shift;
   const int left = min(q8_len(a.src.len, h, a.src.cap), a.budget);
-  const int nt = min(block, left - b * block);
+  const int nt = min(kGatherTok, left - t0);
   if (nt <= 0) return;
-  float sc = 0.f;
-  if (tid < 128) {
-    if (tid < nt) {
-      const int src = a.kept[static_cast<size_t>(h) * a.budget + b * block + tid];
-      s_src[tid] = src;
-      sc = (kv ? a.src.vs : a.src.ks)[static_cast<size_t>(h) * (a.src.cap / block) + src / block];
-      if (kv == 0 && a.to_mass)
-        a.to_mass[static_cast<size_t>(h) * a.cap + b * block + tid] = a.mass[static_cast<size_t>(h) * a.src.cap + src];
-    }
-    float mx = sc;
+  constexpr int kW = D / 16;                              // 16-byte words per row
+  constexpr int kN = kGatherTok * kW * 2 / kGatherThreads;  // words per thread, K's and V's
+  const size_t from = static_cast<size_t>(h) * a.src.cap;
+  const size_t blocks = static_cast<size_t>(h) * (a.src.cap >> shift), to_blocks = static_cast<size_t>(h) * (a.cap >> shift);
+  if (tid < nt) s_src[tid] = a.kept[static_cast<size_t>(h) * a.budget + t0 + tid];
+  __syncthreads();
+  // every row's words, in flight over the scales
+  uint4 w[kN];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if ((tid & 31) == 0) s_max[tid >> 5] = mx;
+  for (int u = 0; u < kN; ++u) {
+    const int i = (tid + u * kGatherThreads) % (kGatherTok * kW);
+    const uint8_t* base = u < kN / 2 ? a.src.K : a.src.V;
+    if (i / kW < nt) w[u] = __ldg(reinterpret_cast<const uint4*>(base + (from + s_src[i / kW]) * D) + i % kW);
+  }
+  const int tok = tid & (kGatherTok - 1), kv = tid / kGatherTok;
+  if (tok < nt) {
+    const int src = s_src[tok];
+    s_scale[kv][tok] = __ldg((kv ? a.src.vs : a.src.ks) + blocks + (src >> shift));
+    if (kv == 0 && a.to_mass) a.to_mass[static_cast<size_t>(h) * a.cap + t0 + tok] = __ldg(a.mass + from + src);
   }
   __syncthreads();
-  const float to = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
-  if (tid < nt) s_ratio[tid] = sc / to;
-  __syncthreads();
-  const uint8_t* from = (kv ? a.src.V : a.src.K) + static_cast<size_t>(h) * a.src.cap * d;
-  uint4* dst = reinterpret_cast<uint4*>((kv ? a.V : a.K) + (static_cast<size_t>(h) * a.cap + b * block) * d);
-  const int words = d / 16;
-  constexpr int kFlight = 4;
-  for (int base = tid; base < nt * words; base += kGatherThreads * kFlight) {
-    uint4 w[kFlight];
-#pragma unroll
-    for (int u = 0; u < kFlight; ++u) {
-      const int i = base + u * kGatherThreads;
-      if (i < nt * words)
-        w[u] = __ldg(reinterpret_cast<const uint4*>(from + static_cast<size_t>(s_src[i / words]) * d) + i % words);
-    }
-#pragma unroll
-    for (int u = 0; u < kFlight; ++u) {
-      const int i = base + u * kGatherThreads;
-      if (i >= nt * words) continue;
-      const float r = s_ratio[i / words];
-      if (r != 1.f) w[u] = make_uint4(rescale4(w[u].x, r), rescale4(w[u].y, r), rescale4(w[u].z, r), rescale4(w[u].w, r));
-      dst[i] = w[u];
-    }
+  const int nb = (nt + (1 << shift) - 1) >> shift;
+  if (tok < nb) {
+    float mx = 0.f;
+    const int end = min((tok + 1) << shift, nt);
+    for (int i = tok << shift; i < end; ++i) mx = fmaxf(mx, s_scale[kv][i]);
+    s_to[kv][tok] = mx;
+    (kv ? a.vs : a.ks)[to_blocks + (t0 >> shift) + tok] = mx;
   }
-  if (tid == 0) (kv ? a.vs : a.ks)[static_cast<size_t>(h) * (a.cap / block) + b] = to;
+  __syncthreads();
+  const size_t to = (static_cast<size_t>(h) * a.cap + t0) * D;
+#pragma unroll
+  for (int u = 0; u < kN; ++u) {
+    const int i = (tid + u * kGatherThreads) % (kGatherTok * kW), row = i / kW;
+    if (row >= nt) continue;
+    const int half = u < kN / 2 ? 0 : 1;
+    const float s = s_scale[half][row], big = s_to[half][row >> shift];
+    if (s != big) {
+      const float r = s / big;
+      w[u] = make_uint4(rescale4(w[u].x, r), rescale4(w[u].y, r), rescale4(w[u].z, r), rescale4(w[u].w, r));
+    }
+    reinterpret_cast<uint4*>((half ? a.V : a.K) + to)[i] = w[u];
+  }
 }
 
 }  // namespace
@@ -259,8 +263,9 @@ cudaError_t launch_q8_evict(const Q8EvictArgs& a, cudaStream_t st) {
   }
   if (e != cudaSuccess) return e;
   LaunchTrace trace("q8_gather_kernel", st);
-  const int blocks = (a.budget + a.src.block - 1) / a.src.block;
-  return launch_pdl(q8_gather_kernel, dim3(blocks, a.src.H, 2), dim3(kGatherThreads), 0, st, a);
+  const dim3 grid((a.budget + kGatherTok - 1) / kGatherTok, a.src.H);
+  return a.src.d == 128 ? launch_pdl(q8_gather_kernel<128>, grid, dim3(kGatherThreads), 0, st, a)
+                        : launch_pdl(q8_gather_kernel<64>, grid, dim3(kGatherThreads), 0, st, a);
 }
 
 }  // namespace kvb

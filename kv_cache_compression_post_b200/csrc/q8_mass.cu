@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mass_kernel(const __grid_const
       const int n = q8_len(a.c.len, p.h, a.c.cap);
       const int key = p.rb * kBlock + t * kRowTile + r;
       const bool mine = t < row_tiles(p);
-      const float ks = __ldg(a.c.ks + static_cast<size_t>(p.h) * (a.c.cap / a.c.block) + min(key, n - 1) / a.c.block);
+      const float ks = __ldg(a.c.ks + static_cast<size_t>(p.h) * (a.c.cap >> a.c.shift) + (min(key, n - 1) >> a.c.shift));
       const float2 ks2 = make_float2(ks, ks);
       float2 sum = make_float2(0.f, 0.f);
       for (int c = p.c0; c < p.c1; ++c, ++g) {

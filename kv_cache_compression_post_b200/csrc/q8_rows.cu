@@ -1,18 +1,21 @@
 // Attention and attention weights over the 8-bit cache for a few rows per head: the
 // single-token form, and query heads that share a K/V head.
 //
-// Reading the cache once is the bound (2 bytes per token and channel pair), so the
-// work is split over its tokens (Q8Split), a warp takes 32 tokens at a time straight
-// from global memory into the fragments of mma.sync.m16n8k16 (16 rows x 8 tokens), and
-// no token passes through shared memory.  What the layout relies on: a contraction
-// may run over the channels, and over the tokens, in any order that both operands
-// share.  Lane (g, t) = (lane / 4, lane % 4) loads 16 contiguous bytes of token g's
-// K row and uses them as four MMA steps, so Q is fetched in that order of channels;
-// it loads 16 contiguous bytes of V for the four tokens its P columns stand for, and
-// output column n of MMA j is channel 16 n + j.  Codes widen to fp16 exactly, two per
-// instruction, and Q enters as fp16 times a power of two per row (bf16 has 8 bits,
-// fp16 11, so nothing is lost above 2^-14 of the row's largest).
-//
+// Reading the cache once is the bound (2 bytes per token and channel), so the work is
+// split over its tokens (Q8Split) and every warp streams 32 tokens at a time through a
+// ring of its own in shared memory (cp.async, no barrier between warps) into the
+// fragments of mma.sync.  What the layout relies on: a contraction may run over the
+// channels, and over the tokens, in any order that both operands share.  Lane (g, t) =
+// (lane / 4, lane % 4) takes 16 contiguous bytes of token g's K row and uses them as two
+// m16n8k32 steps, so Q is fetched in that order of channels; it takes 16 contiguous bytes
+// of V for the four tokens its P columns stand for, and output column n of MMA j is
+// channel 16 n + j.
+// K's codes are multiplied as they lie, against two E4M3 parts of each query element
+// (q = hi + lo, exact down to 2^-17 of the row's largest; up to eight rows carry them as
+// the upper and lower half of one 16-row operand).  Widening a pair of codes to fp16
+// takes 8 clk of a scheduler's ALU: with K widened, too, that and not the memory was the
+// bound (8 heads x 8 rows x 98304 tokens on average: 73 us).  V is widened, exactly, and
+// P is fp16.
 // Softmax in the log2 domain.  With ks, vs the scales of a token's block,
 //     x = (q.k) ks scale log2 e,   P = 2^(x + log2 vs - m + kPBias),
 // m the running maximum of x + log2 vs: V's scale rides in the exponent at no cost,
@@ -34,6 +37,7 @@ constexpr int kSub = 32;     // tokens a warp takes at a time
 constexpr int kRows = 16;    // rows per row tile
 constexpr float kPBias = 8.f;
 constexpr int kMinTiles = 4;  // a CTA's share: one 32-token step for each warp
+constexpr int kRing = 3;      // stages of a warp's ring
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -51,17 +55,27 @@ __device__ __forceinline__ float quad_sum(float v) {
   return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
 
-// The A fragments of one 16-row tile: row g and g + 8 of this lane, channels 64 hb +
-// 16 t .. + 15 in the order the K bytes come.  coef[i]: what turns a raw dot product
-// of row g + 8 i into log2 units (but for the token's scale).
-template <int D>
+__device__ __forceinline__ void mma_16832_e4m3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The A fragments of one row tile: the two E4M3 parts of rows g (and g + 8), channels
+// 64 hb + 16 t .. + 15 in the order the K bytes come.  FEW (at most eight rows): the
+// lower half of the operand holds the second parts; otherwise they are an operand of
+// their own.  coef[i]: what turns a raw dot product of row g + 8 i into log2 units (but
+// for the token's scale).
+template <int D, bool FEW>
 struct QFrag {
-  uint32_t a[D / 16][4];
-  float coef[2];
+  static constexpr int kI = FEW ? 1 : 2;
+  uint32_t a[D / 32][FEW ? 1 : 2][4];  // [32-channel step][part][register]
+  float coef[kI];
 
   __device__ __forceinline__ void load(const __nv_bfloat16* Q, int rows, float scale, int g, int t) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kI; ++i) {
       const int row = g + 8 * i;
       uint4 w[D / 32];
 #pragma unroll
@@ -82,29 +96,82 @@ struct QFrag {
         }
       }
       mx = quad_max(mx);
-      const int e = min(max(exponent_of(mx), -100), 126);
+      const int e = max(exponent_of(mx), -100) - 7;  // mx 2^-e in [2^7, 2^8)
       const float down = pow2f(-e);
       coef[i] = pow2f(e) * scale * kLog2e;
+      // eight channels: one step; its first four to register i, the others to i + 2
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) {
-        // 8 channels: two MMA steps, (0,1) and (2,3) of each to registers i, i + 2
         const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
 #pragma unroll
-        for (int e2 = 0; e2 < 4; ++e2) {
-          const float2 f = unpack_bf16x2(u[e2]);
-          a[k * 2 + (e2 >> 1)][i + 2 * (e2 & 1)] = pack_f16x2(f.x * down, f.y * down);
+        for (int half = 0; half < 2; ++half) {
+          uint32_t hi = 0u, lo = 0u;
+#pragma unroll
+          for (int e2 = 0; e2 < 2; ++e2) {
+            const float2 f = unpack_bf16x2(u[half * 2 + e2]);
+            // an infinite element becomes a NaN: its row is NaN, as its scores would be
+            const float x = fabsf(f.x) <= 3.4e38f ? f.x * down : NAN, y = fabsf(f.y) <= 3.4e38f ? f.y * down : NAN;
+            const uint32_t c = f32x2_to_e4m3x2(x, y);
+            const float2 b = e4m3x2_to_f32x2(c);
+            hi |= c << (16 * e2);
+            lo |= f32x2_to_e4m3x2(x - b.x, y - b.y) << (16 * e2);
+          }
+          if constexpr (FEW) {
+            a[k][0][2 * half] = hi;
+            a[k][0][2 * half + 1] = lo;
+          } else {
+            a[k][0][i + 2 * half] = hi;
+            a[k][1][i + 2 * half] = lo;
+          }
         }
       }
     }
   }
 };
 
-// Raw K words of 32 tokens from `kb` (token index in the head), rows past the last
-// held token read the last one (masked later).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Where the 16-byte unit c of row `row` lies in a stage: turned so that the fragments'
+// reads below meet no bank twice (rows of 128 bytes).
+template <int D>
+__device__ __forceinline__ int k_unit(int row, int c) { return D == 128 ? c ^ ((row & 1) << 2) : c; }
+template <int D>
+__device__ __forceinline__ int v_unit(int row, int c) { return D == 128 ? c ^ (row & 6) : c ^ ((row >> 1) & 3); }
+
+// Fetch K and V rows of 32 tokens from `kb` (token index in the head) into a stage;
+// rows past the last held token repeat it (masked later).
+template <int D>
+__device__ __forceinline__ void fetch(uint32_t stage, const uint8_t* K, const uint8_t* V, int kb, int last, int lane) {
+  constexpr int kU = D / 16;
+#pragma unroll
+  for (int i = 0; i < kU; ++i) {
+    const int row = (lane + 32 * i) / kU, c = (lane + 32 * i) % kU;
+    const size_t at = static_cast<size_t>(min(kb + row, last)) * D + c * 16;
+    cp_async16(stage + row * D + k_unit<D>(row, c) * 16, K + at);
+    cp_async16(stage + 32 * D + row * D + v_unit<D>(row, c) * 16, V + at);
+  }
+}
+
+// K words of 32 tokens
 template <int D>
 struct KWords {
   uint4 w[4][D / 64];
-  __device__ __forceinline__ void load(const uint8_t* K, int kb, int last, int g, int t) {
+  __device__ __forceinline__ void load(const uint8_t* stage, int g, int t) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int hb = 0; hb < D / 64; ++hb)
+        w[j][hb] = *reinterpret_cast<const uint4*>(stage + (8 * j + g) * D + k_unit<D>(g, hb * 4 + t) * 16);
+  }
+  // straight from global memory, for the weights, which read K once and nothing else
+  __device__ __forceinline__ void load_global(const uint8_t* K, int kb, int last, int g, int t) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int key = min(kb + 8 * j + g, last);
@@ -113,8 +180,10 @@ struct KWords {
         w[j][hb] = __ldg(reinterpret_cast<const uint4*>(K + static_cast<size_t>(key) * D + hb * 64 + t * 16));
     }
   }
-  // s[j]: raw dot products of rows g (0, 1) and g + 8 (2, 3) with tokens 8 j + 2 t, + 1
-  __device__ __forceinline__ void dots(const QFrag<D>& q, float (&s)[4][4]) const {
+  // s[j]: raw dot products of rows g (0, 1) and, unless FEW, g + 8 (2, 3) with tokens
+  // 8 j + 2 t, + 1
+  template <bool FEW>
+  __device__ __forceinline__ void dots(const QFrag<D, FEW>& q, float (&s)[4][4]) const {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
 #pragma unroll
@@ -123,7 +192,14 @@ struct KWords {
       for (int hb = 0; hb < D / 64; ++hb) {
         const uint32_t u[4] = {w[j][hb].x, w[j][hb].y, w[j][hb].z, w[j][hb].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mma_16816(s[j], q.a[hb * 4 + i], e4m3x2_to_f16x2(u[i]), e4m3x2_to_f16x2(u[i] >> 16));
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int part = 0; part < (FEW ? 1 : 2); ++part)
+            mma_16832_e4m3(s[j], q.a[hb * 2 + i][part], u[2 * i], u[2 * i + 1]);
+      }
+      if constexpr (FEW) {
+        s[j][0] += s[j][2];
+        s[j][1] += s[j][3];
       }
     }
   }
@@ -133,18 +209,18 @@ template <int D>
 struct VWords {
   static constexpr int kW = D / 32;  // 32-bit words per lane and token (8 lanes per row)
   uint32_t w[2][4][kW];
-  __device__ __forceinline__ void load(const uint8_t* V, int kb, int last, int g, int t) {
+  __device__ __forceinline__ void load(const uint8_t* stage, int g, int t) {
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int key = min(kb + 16 * u + 2 * t + (k & 1) + 8 * (k >> 1), last);
-        const uint8_t* p = V + static_cast<size_t>(key) * D + g * (D / 8);
+        const int row = 16 * u + 2 * t + (k & 1) + 8 * (k >> 1);
+        const uint8_t* p = stage + row * D;
         if constexpr (D == 128) {
-          const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
+          const uint4 x = *reinterpret_cast<const uint4*>(p + v_unit<D>(row, g) * 16);
           w[u][k][0] = x.x, w[u][k][1] = x.y, w[u][k][2] = x.z, w[u][k][3] = x.w;
         } else {
-          const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+          const uint2 x = *reinterpret_cast<const uint2*>(p + v_unit<D>(row, g >> 1) * 16 + (g & 1) * 8);
           w[u][k][0] = x.x, w[u][k][1] = x.y;
         }
       }
@@ -173,18 +249,22 @@ struct RowsShared {
   float m[kWarps][kRows], l[kWarps][kRows];
 };
 
-template <int D>
+template <int D, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1) q8_attend_rows_kernel(const Q8AttendArgs a) {
+  constexpr int kI = FEW ? 1 : 2;  // rows of a lane: g, g + 8
   extern __shared__ uint8_t smem[];
   __shared__ Q8Sched sch;
-  RowsShared<D>& sh = *reinterpret_cast<RowsShared<D>*>(smem);
+  RowsShared<D>& sh = *reinterpret_cast<RowsShared<D>*>(smem);  // over the rings, once they are done with
   pdl_wait();
   pdl_trigger();
   const int nrt = (a.Nq + kRows - 1) / kRows;
   q8_build_sched(&sch, a.c.len, a.c.cap, a.c.H, nrt, kTile, 1, 1, gridDim.x, kMinTiles);
   Q8Split S{&sch, a.c.H, nrt, 1, 1};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int blocks = a.c.cap / a.c.block;
+  const int blocks = a.c.cap >> a.c.shift;
+  constexpr int kStage = 64 * D;  // K and V of 32 tokens
+  uint8_t* ring = smem + static_cast<size_t>(warp) * kRing * kStage;
+  const uint32_t ring32 = smem_u32(ring);
   Q8Walk walk;
   walk.init(S, blockIdx.x);
   Q8Piece pc;
@@ -197,45 +277,77 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_rows_kernel(const Q8Att
     const uint8_t* V = a.c.V + static_cast<size_t>(pc.h) * a.c.cap * D;
     const float* ks = a.c.ks + static_cast<size_t>(pc.h) * blocks;
     const float* vs = a.c.vs + static_cast<size_t>(pc.h) * blocks;
-    QFrag<D> q;
+    constexpr int kHop = kWarps * kSub;
+    const int first = pc.j0 * kTile + warp * kSub;
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i) {
+      if (first + i * kHop < end) fetch<D>(ring32 + i * kStage, K, V, first + i * kHop, n - 1, lane);
+      cp_async_commit();
+    }
+    // the scales of a step's two 16-token halves, a step ahead
+    float nk[2], nv[2];
+    auto scales = [&](int kb) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int b = min(kb + 16 * u, n - 1) >> a.c.shift;
+        nk[u] = __ldg(ks + b);
+        nv[u] = __ldg(vs + b);
+      }
+    };
+    scales(first);
+    QFrag<D, FEW> q;
     q.load(static_cast<const __nv_bfloat16*>(a.Q) + row0 * D, rows, a.scale, g, t);
     float o[D / 8][4];
 #pragma unroll
     for (int j = 0; j < D / 8; ++j)
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[j][k] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    for (int kb = pc.j0 * kTile + warp * kSub; kb < end; kb += kWarps * kSub) {
+    float m[kI], l[kI];
+#pragma unroll
+    for (int i = 0; i < kI; ++i) m[i] = -INFINITY, l[i] = 0.f;
+    int stage = 0;
+    for (int kb = first; kb < end; kb += kHop) {
+      __syncwarp();  // every lane is done with the stage that is fetched into next
+      {
+        const int ahead = kb + (kRing - 1) * kHop, st = stage == 0 ? kRing - 1 : stage - 1;
+        if (ahead < end) fetch<D>(ring32 + st * kStage, K, V, ahead, n - 1, lane);
+        cp_async_commit();
+      }
+      cp_async_wait<kRing - 1>();
+      __syncwarp();
       KWords<D> kw;
-      VWords<D> vw;
-      kw.load(K, kb, n - 1, g, t);
-      vw.load(V, kb, n - 1, g, t);
+      kw.load(ring + stage * kStage, g, t);
       float kf[2], lv[2], iv[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int b = min(kb + 16 * u, n - 1) / a.c.block;
-        const float v = __ldg(vs + b);
-        kf[u] = __ldg(ks + b);
-        lv[u] = log2f(v);
-        iv[u] = 1.f / v;
+        kf[u] = nk[u];
+        lv[u] = log2f(nv[u]);
+        iv[u] = 1.f / nv[u];
       }
+      if (kb + kHop < end) scales(kb + kHop);
       float s[4][4];
-      kw.dots(q, s);
-      float mt[2] = {-INFINITY, -INFINITY};
+      kw.template dots<FEW>(q, s);
+      float mt[kI];
+#pragma unroll
+      for (int i = 0; i < kI; ++i) mt[i] = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 2 * kI; ++k) {
           const int key = kb + 8 * j + 2 * t + (k & 1);
           const float x = fmaf(s[j][k], q.coef[k >> 1] * kf[j >> 1], lv[j >> 1]);
           s[j][k] = key < end ? x : -INFINITY;
           mt[k >> 1] = fmaxf(mt[k >> 1], s[j][k]);
         }
-      mt[0] = quad_max(mt[0]);
-      mt[1] = quad_max(mt[1]);
-      if (__any_sync(0xffffffffu, mt[0] > m[0] || mt[1] > m[1])) {
+      bool moved = false;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < kI; ++i) {
+        mt[i] = quad_max(mt[i]);
+        moved |= mt[i] > m[i];
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int i = 0; i < kI; ++i) {
           const float mn = fmaxf(m[i], mt[i]);
           const float al = mn == -INFINITY ? 1.f : exp2f(m[i] - mn);
           m[i] = mn;
@@ -247,37 +359,39 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_rows_kernel(const Q8Att
           }
         }
       }
-      // a row whose every score is -inf so far (NaN queries aside) keeps P = 0
-      const float b0 = (m[0] == -INFINITY ? 0.f : -m[0]) + kPBias, b1 = (m[1] == -INFINITY ? 0.f : -m[1]) + kPBias;
+      VWords<D> vw;
+      vw.load(ring + stage * kStage + 32 * D, g, t);
+      stage = stage == kRing - 1 ? 0 : stage + 1;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        float r0 = 0.f, r1 = 0.f;
-        uint32_t p[4];
+        uint32_t p[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int j = 2 * u + i;
-          const float p0 = ex2_approx(s[j][0] + b0), p1 = ex2_approx(s[j][1] + b0);
-          const float p2 = ex2_approx(s[j][2] + b1), p3 = ex2_approx(s[j][3] + b1);
-          r0 += p0 + p1;
-          r1 += p2 + p3;
-          p[2 * i] = pack_f16x2(p0, p1);
-          p[2 * i + 1] = pack_f16x2(p2, p3);
+        for (int i = 0; i < kI; ++i) {
+          // a row whose every score is -inf so far (NaN queries aside) keeps P = 0
+          const float b = (m[i] == -INFINITY ? 0.f : -m[i]) + kPBias;
+          float r = 0.f;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float x = ex2_approx(s[2 * u + j][2 * i] + b), y = ex2_approx(s[2 * u + j][2 * i + 1] + b);
+            r += x + y;
+            p[2 * j + i] = pack_f16x2(x, y);
+          }
+          l[i] = fmaf(r, iv[u], l[i]);
         }
-        l[0] = fmaf(r0, iv[u], l[0]);
-        l[1] = fmaf(r1, iv[u], l[1]);
         vw.accumulate(u, p, o);
       }
     }
     // merge the eight warps: maxima first, then every output weighted by its warp
-    l[0] = quad_sum(l[0]);
-    l[1] = quad_sum(l[1]);
-    __syncthreads();  // the previous piece's merge is done with the shared memory
+#pragma unroll
+    for (int i = 0; i < kI; ++i) l[i] = quad_sum(l[i]);
+    cp_async_wait<0>();
+    __syncthreads();  // every warp is done with its ring
     if (t == 0) {
-      sh.m[warp][g] = m[0], sh.m[warp][g + 8] = m[1];
-      sh.l[warp][g] = l[0], sh.l[warp][g + 8] = l[1];
+#pragma unroll
+      for (int i = 0; i < kI; ++i) sh.m[warp][g + 8 * i] = m[i], sh.l[warp][g + 8 * i] = l[i];
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 2 * kI; ++k) {
       const int row = g + 8 * (k >> 1);
       if (row >= rows) continue;
       float* to = &sh.o[warp][row][(2 * t + (k & 1)) * (D / 8)];
@@ -317,63 +431,93 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_rows_kernel(const Q8Att
         }
       }
     }
+    __syncthreads();  // the merge is done with the shared memory
   }
 }
 
-// Units cut into pieces, and heads without tokens: one CTA per (row tile, head).
-// Every CTA lays out the same split again (the lengths have not changed).
+// Units cut into pieces, and heads without tokens: one CTA per (row tile, head).  Every
+// CTA lays out the same split again (the lengths have not changed), turns the pieces'
+// maxima and sums, all fetched at once, into one weight per (row, piece), and adds the
+// pieces' outputs in their order with eight fetches in flight.
+constexpr int kMergeThreads = 256;
 template <int D, typename T>
-__global__ void __launch_bounds__(128) q8_merge_rows_kernel(const Q8AttendArgs a, int tile_rows, int tile, int grid,
-                                                           int min_tiles, float bias) {
+__global__ void __launch_bounds__(kMergeThreads) q8_merge_rows_kernel(const Q8AttendArgs a, int tile_rows, int tile,
+                                                                      int grid, int min_tiles, float bias) {
   __shared__ Q8Sched sch;
+  __shared__ float s_w[kRows][kQ8MaxCtas], s_l[kRows][kQ8MaxCtas];
   pdl_wait();
   pdl_trigger();
   const int nrt = (a.Nq + tile_rows - 1) / tile_rows;
   q8_build_sched(&sch, a.c.len, a.c.cap, a.c.H, nrt, tile, 1, 1, grid, min_tiles);
   Q8Split S{&sch, a.c.H, nrt, 1, 1};
-  const int r = blockIdx.x, h = blockIdx.y;
+  const int r = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
   const int rows = min(tile_rows, a.Nq - r * tile_rows);
   const size_t row0 = static_cast<size_t>(h) * a.Nq + r * tile_rows;
-  const size_t slot_size = static_cast<size_t>(kRows) * D + 2 * kRows;
+  constexpr size_t kSlot = static_cast<size_t>(kRows) * D + 2 * kRows;
   T* O = static_cast<T*>(a.O);
   auto put = [&](int row, int c, float4 v) {
     T* p = O + (row0 + row) * D + c;
     if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     else *reinterpret_cast<float4*>(p) = v;
   };
-  Q8Piece pc;
-  const bool empty = sch.T[h] == 0;
-  if (!empty) {
-    q8_unit_pieces(S, h, r, pc);
-    if (pc.npieces == 1) return;
+  if (sch.T[h] == 0) {
+    for (int i = tid; i < rows * (D / 4); i += kMergeThreads) put(i / (D / 4), (i % (D / 4)) * 4, make_float4(0.f, 0.f, 0.f, 0.f));
+    if (a.lse)
+      for (int i = tid; i < rows; i += kMergeThreads) a.lse[row0 + i] = -INFINITY;
+    return;
   }
-  for (int i = threadIdx.x; i < rows * (D / 4); i += blockDim.x) {
-    const int row = i / (D / 4), c = (i % (D / 4)) * 4;
-    if (empty) {
-      put(row, c, make_float4(0.f, 0.f, 0.f, 0.f));
-      if (a.lse && c == 0) a.lse[row0 + row] = -INFINITY;
-      continue;
-    }
+  Q8Piece pc;
+  q8_unit_pieces(S, h, r, pc);
+  const int np = pc.npieces;
+  if (np == 1) return;
+  const float* first = a.part + static_cast<size_t>(pc.cfirst * 2 + pc.wfirst) * kSlot;
+  const float* rest = a.part + static_cast<size_t>(pc.cfirst) * 2 * kSlot;  // piece k > 0: slot 0 of CTA cfirst + k
+  auto slot = [&](int k) { return k == 0 ? first : rest + static_cast<size_t>(k) * 2 * kSlot; };
+  for (int i = tid; i < rows * np; i += kMergeThreads) {
+    const int row = i / np, k = i - row * np;
+    s_w[row][k] = __ldg(slot(k) + kRows * D + row);
+    s_l[row][k] = __ldg(slot(k) + kRows * D + kRows + row);
+  }
+  __syncthreads();
+  const int warp = tid >> 5, lane = tid & 31;
+  for (int row = warp; row < rows; row += kMergeThreads / 32) {
     float M = -INFINITY;
-    for (int k = 0; k < pc.npieces; ++k) {
-      const float* s = a.part + static_cast<size_t>((pc.cfirst + k) * 2 + (k ? 0 : pc.wfirst)) * slot_size;
-      M = fmaxf(M, s[kRows * D + row]);
-    }
+    for (int k = lane; k < np; k += 32) M = fmaxf(M, s_w[row][k]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     float L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < pc.npieces; ++k) {
-      const float* s = a.part + static_cast<size_t>((pc.cfirst + k) * 2 + (k ? 0 : pc.wfirst)) * slot_size;
-      const float f = M == -INFINITY ? 1.f : exp2f(s[kRows * D + row] - M);
-      const float4 x = *reinterpret_cast<const float4*>(s + row * D + c);
-      L = fmaf(f, s[kRows * D + kRows + row], L);
-      acc.x = fmaf(f, x.x, acc.x);
-      acc.y = fmaf(f, x.y, acc.y);
-      acc.z = fmaf(f, x.z, acc.z);
-      acc.w = fmaf(f, x.w, acc.w);
+    for (int k = lane; k < np; k += 32) {
+      const float f = M == -INFINITY ? 1.f : exp2f(s_w[row][k] - M);
+      s_w[row][k] = f;
+      L = fmaf(f, s_l[row][k], L);
     }
-    const float inv = 1.f / L;
+    L = warp_sum(L);
+    if (lane == 0) {
+      s_l[row][0] = 1.f / L;
+      if (a.lse) a.lse[row0 + row] = (M - bias + log2f(L)) * kLn2;
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < rows * (D / 4); i += kMergeThreads) {
+    const int row = i / (D / 4), c = (i % (D / 4)) * 4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < np; k0 += 8) {
+      float4 x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (k0 + u < np) x[u] = __ldg(reinterpret_cast<const float4*>(slot(k0 + u) + row * D + c));
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (k0 + u >= np) continue;
+        const float f = s_w[row][k0 + u];
+        acc.x = fmaf(f, x[u].x, acc.x);
+        acc.y = fmaf(f, x[u].y, acc.y);
+        acc.z = fmaf(f, x[u].z, acc.z);
+        acc.w = fmaf(f, x[u].w, acc.w);
+      }
+    }
+    const float inv = s_l[row][0];
     put(row, c, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-    if (a.lse && c == 0) a.lse[row0 + row] = (M - bias + log2f(L)) * kLn2;
   }
 }
 
@@ -427,7 +571,7 @@ __global__ void __launch_bounds__(kF32Threads) q8_attend_f32_kernel(const Q8Atte
   q8_build_sched(&sch, a.c.len, a.c.cap, a.c.H, nrt, kTile, 1, 1, gridDim.x, kMinTiles);
   Q8Split S{&sch, a.c.H, nrt, 1, 1};
   const int grp = threadIdx.x >> 3, sub = threadIdx.x & 7;
-  const int blocks = a.c.cap / a.c.block;
+  const int blocks = a.c.cap >> a.c.shift;
   Q8Walk walk;
   walk.init(S, blockIdx.x);
   Q8Piece pc;
@@ -455,8 +599,8 @@ __global__ void __launch_bounds__(kF32Threads) q8_attend_f32_kernel(const Q8Atte
       float kf[D / 8], vf[D / 8];
       load_codes<D>(a.c.K + at + static_cast<size_t>(kc) * D, kf);
       load_codes<D>(a.c.V + at + static_cast<size_t>(kc) * D, vf);
-      const float ks = __ldg(a.c.ks + static_cast<size_t>(pc.h) * blocks + kc / a.c.block);
-      const float vs = __ldg(a.c.vs + static_cast<size_t>(pc.h) * blocks + kc / a.c.block);
+      const float ks = __ldg(a.c.ks + static_cast<size_t>(pc.h) * blocks + (kc >> a.c.shift));
+      const float vs = __ldg(a.c.vs + static_cast<size_t>(pc.h) * blocks + (kc >> a.c.shift));
 #pragma unroll
       for (int r = 0; r < kF32Rows; ++r) {
         float s = 0.f;
@@ -517,40 +661,41 @@ __global__ void __launch_bounds__(kF32Threads) q8_attend_f32_kernel(const Q8Atte
 // mass[k] = decay prev[k] + sum over rows of 2^(x - lse log2 e): a token's weight is
 // whole within its warp, so there is nothing to split or merge, and the rows are added
 // in one fixed order.  Reads K once per 16 rows (the first time from memory).
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1) q8_mass_rows_kernel(const Q8MassArgs a) {
+template <int D, bool FEW>
+__global__ void __launch_bounds__(kThreads) q8_mass_rows_kernel(const Q8MassArgs a) {
+  constexpr int kI = FEW ? 1 : 2;
   pdl_wait();
   pdl_trigger();
   const int h = blockIdx.y;
   const int n = q8_len(a.c.len, h, a.c.cap);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const uint8_t* K = a.c.K + static_cast<size_t>(h) * a.c.cap * D;
-  const float* ks = a.c.ks + static_cast<size_t>(h) * (a.c.cap / a.c.block);
+  const float* ks = a.c.ks + static_cast<size_t>(h) * (a.c.cap >> a.c.shift);
   for (int kb = (blockIdx.x * kWarps + warp) * kSub; kb < n; kb += gridDim.x * kWarps * kSub) {
     KWords<D> kw;
-    kw.load(K, kb, n - 1, g, t);
+    kw.load_global(K, kb, n - 1, g, t);
     float kf[2], w[4][2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) kf[u] = __ldg(ks + min(kb + 16 * u, n - 1) / a.c.block);
+    for (int u = 0; u < 2; ++u) kf[u] = __ldg(ks + (min(kb + 16 * u, n - 1) >> a.c.shift));
 #pragma unroll
     for (int j = 0; j < 4; ++j) w[j][0] = w[j][1] = 0.f;
     for (int r0 = 0; r0 < a.Nq; r0 += kRows) {
       const size_t row0 = static_cast<size_t>(h) * a.Nq + r0;
       const int rows = min(kRows, a.Nq - r0);
-      QFrag<D> q;
+      QFrag<D, FEW> q;
       q.load(static_cast<const __nv_bfloat16*>(a.Q) + row0 * D, rows, a.scale, g, t);
-      float z[2];
+      float z[kI];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < kI; ++i) {
         const float v = g + 8 * i < rows ? a.lse[row0 + g + 8 * i] : -INFINITY;
         z[i] = v == -INFINITY ? -INFINITY : -v * kLog2e;  // a row of lse -inf weighs nothing
       }
       float s[4][4];
-      kw.dots(q, s);
+      kw.template dots<FEW>(q, s);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) w[j][k & 1] += ex2_approx(fmaf(s[j][k], q.coef[k >> 1] * kf[j >> 1], z[k >> 1]));
+        for (int k = 0; k < 2 * kI; ++k) w[j][k & 1] += ex2_approx(fmaf(s[j][k], q.coef[k >> 1] * kf[j >> 1], z[k >> 1]));
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -568,54 +713,78 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mass_rows_kernel(const Q8MassA
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) q8_mass_f32_kernel(const Q8MassArgs a) {
+// f32: eight lanes per token as in the attention, kF32Keys tokens per group of lanes at a
+// time, so that a row's elements are fetched once for all of them; a single row (ONE) is
+// held in registers for all tokens.  The loads of a round do not wait on one another.
+constexpr int kF32Keys = 4;
+template <int D, bool ONE>
+__global__ void __launch_bounds__(kThreads, 2) q8_mass_f32_kernel(const Q8MassArgs a) {
   pdl_wait();
   pdl_trigger();
   const int h = blockIdx.y;
   const int n = q8_len(a.c.len, h, a.c.cap);
   const int grp = threadIdx.x >> 3, sub = threadIdx.x & 7;
   constexpr int kGroups = kThreads / 8;
-  const int base = blockIdx.x * kGroups;
-  for (int k0 = base; k0 < n; k0 += gridDim.x * kGroups) {
-    const int key = k0 + grp, kc = min(key, n - 1);
-    float kf[D / 8];
-    load_codes<D>(a.c.K + (static_cast<size_t>(h) * a.c.cap + kc) * D + sub * (D / 8), kf);
-    const float mul = __ldg(a.c.ks + static_cast<size_t>(h) * (a.c.cap / a.c.block) + kc / a.c.block) * a.scale;
-    float w = 0.f;
-    for (int r = 0; r < a.Nq; ++r) {
-      const size_t row = static_cast<size_t>(h) * a.Nq + r;
-      float q[D / 8];
-      load_q<D>(static_cast<const float*>(a.Q) + row * D + sub * (D / 8), 1.f, q);
-      float s = 0.f;
+  const float* Q = static_cast<const float*>(a.Q) + static_cast<size_t>(h) * a.Nq * D + sub * (D / 8);
+  const float* lse = a.lse + static_cast<size_t>(h) * a.Nq;
+  const uint8_t* K = a.c.K + static_cast<size_t>(h) * a.c.cap * D + sub * (D / 8);
+  const float* ks = a.c.ks + static_cast<size_t>(h) * (a.c.cap >> a.c.shift);
+  const size_t m0 = static_cast<size_t>(h) * a.c.cap;
+  float q[D / 8], z = 0.f;
+  if constexpr (ONE) {
+    load_q<D>(Q, 1.f, q);
+    z = lse[0];
+  }
+  for (int k0 = blockIdx.x * kGroups * kF32Keys; k0 < n; k0 += gridDim.x * kGroups * kF32Keys) {
+    float kf[kF32Keys][D / 8], mul[kF32Keys], w[kF32Keys];
+    // lane u of the group stores token u's weight, and fetches what it adds to
+    const int mine = k0 + sub * kGroups + grp;
+    float before = 0.f;
+    if (sub < kF32Keys && mine < n && a.prev) before = a.prev[m0 + mine];
 #pragma unroll
-      for (int k = 0; k < D / 8; ++k) s = fmaf(q[k], kf[k], s);
-      const float z = a.lse[row];
-      const float x = octet_sum(s);
-      if (z != -INFINITY) w += expf(fmaf(x, mul, -z));
+    for (int u = 0; u < kF32Keys; ++u) {
+      const int kc = min(k0 + u * kGroups + grp, n - 1);
+      load_codes<D>(K + static_cast<size_t>(kc) * D, kf[u]);
+      mul[u] = __ldg(ks + (kc >> a.c.shift)) * a.scale;
+      w[u] = 0.f;
     }
-    if (sub == 0 && key < n) {
-      const size_t at = static_cast<size_t>(h) * a.c.cap + key;
-      a.mass[at] = a.prev ? fmaf(a.decay, a.prev[at], w) : w;
+    for (int r = 0; r < (ONE ? 1 : a.Nq); ++r) {
+      if constexpr (!ONE) {
+        load_q<D>(Q + static_cast<size_t>(r) * D, 1.f, q);
+        z = lse[r];
+      }
+#pragma unroll
+      for (int u = 0; u < kF32Keys; ++u) {
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) s = fmaf(q[k], kf[u][k], s);
+        const float x = octet_sum(s);
+        if (z != -INFINITY) w[u] += expf(fmaf(x, mul[u], -z));
+      }
+    }
+    if (sub < kF32Keys && mine < n) {
+      const float v = sub == 0 ? w[0] : (sub == 1 ? w[1] : (sub == 2 ? w[2] : w[3]));
+      a.mass[m0 + mine] = a.prev ? fmaf(a.decay, before, v) : v;
     }
   }
 }
 
 int split_grid(int n_sm) { return n_sm < kQ8MaxCtas ? n_sm : kQ8MaxCtas; }
 
-template <int D>
+template <int D, bool FEW>
 cudaError_t attend_rows(const Q8AttendArgs& a, int n_sm, cudaStream_t st) {
   const int grid = split_grid(n_sm);
-  cudaError_t e = cudaFuncSetAttribute(q8_attend_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(sizeof(RowsShared<D>)));
+  constexpr size_t smem = kWarps * kRing * 64 * D > sizeof(RowsShared<D>) ? kWarps * kRing * 64 * D : sizeof(RowsShared<D>);
+  cudaError_t e = cudaFuncSetAttribute(q8_attend_rows_kernel<D, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   {
     LaunchTrace trace("q8_attend_rows_kernel", st);
-    e = launch_pdl(q8_attend_rows_kernel<D>, dim3(grid), dim3(kThreads), sizeof(RowsShared<D>), st, a);
+    e = launch_pdl(q8_attend_rows_kernel<D, FEW>, dim3(grid), dim3(kThreads), smem, st, a);
   }
   if (e != cudaSuccess) return e;
   LaunchTrace trace("q8_merge_rows_kernel", st);
-  return launch_pdl(q8_merge_rows_kernel<D, __nv_bfloat16>, dim3((a.Nq + kRows - 1) / kRows, a.c.H), dim3(128), 0, st, a,
+  return launch_pdl(q8_merge_rows_kernel<D, __nv_bfloat16>, dim3((a.Nq + kRows - 1) / kRows, a.c.H), dim3(kMergeThreads), 0, st, a,
                     static_cast<int>(kRows), static_cast<int>(kTile), grid, static_cast<int>(kMinTiles), static_cast<float>(kPBias));
 }
 
@@ -630,7 +799,7 @@ cudaError_t attend_f32(const Q8AttendArgs& a, int n_sm, cudaStream_t st) {
   }
   if (e != cudaSuccess) return e;
   LaunchTrace trace("q8_merge_rows_kernel", st);
-  return launch_pdl(q8_merge_rows_kernel<D, float>, dim3((a.Nq + kF32Rows - 1) / kF32Rows, a.c.H), dim3(128), 0, st, a,
+  return launch_pdl(q8_merge_rows_kernel<D, float>, dim3((a.Nq + kF32Rows - 1) / kF32Rows, a.c.H), dim3(kMergeThreads), 0, st, a,
                     static_cast<int>(kF32Rows), static_cast<int>(kTile), grid, static_cast<int>(kMinTiles), 0.f);
 }
 
@@ -644,7 +813,8 @@ int mass_blocks(int cap, int per_cta, int H, int n_sm, int waves) {
 }  // namespace
 
 cudaError_t launch_q8_attend_rows(const Q8AttendArgs& a, int n_sm, cudaStream_t st) {
-  return a.c.d == 128 ? attend_rows<128>(a, n_sm, st) : attend_rows<64>(a, n_sm, st);
+  if (a.Nq <= 8) return a.c.d == 128 ? attend_rows<128, true>(a, n_sm, st) : attend_rows<64, true>(a, n_sm, st);
+  return a.c.d == 128 ? attend_rows<128, false>(a, n_sm, st) : attend_rows<64, false>(a, n_sm, st);
 }
 cudaError_t launch_q8_attend_f32(const Q8AttendArgs& a, int n_sm, cudaStream_t st) {
   return a.c.d == 128 ? attend_f32<128>(a, n_sm, st) : attend_f32<64>(a, n_sm, st);
@@ -652,14 +822,20 @@ cudaError_t launch_q8_attend_f32(const Q8AttendArgs& a, int n_sm, cudaStream_t s
 cudaError_t launch_q8_mass_rows(const Q8MassArgs& a, int n_sm, cudaStream_t st) {
   const dim3 grid(mass_blocks(a.c.cap, kWarps * kSub, a.c.H, n_sm, 2), a.c.H);
   LaunchTrace trace("q8_mass_rows_kernel", st);
-  return a.c.d == 128 ? launch_pdl(q8_mass_rows_kernel<128>, grid, dim3(kThreads), 0, st, a)
-                      : launch_pdl(q8_mass_rows_kernel<64>, grid, dim3(kThreads), 0, st, a);
+  if (a.Nq <= 8)
+    return a.c.d == 128 ? launch_pdl(q8_mass_rows_kernel<128, true>, grid, dim3(kThreads), 0, st, a)
+                        : launch_pdl(q8_mass_rows_kernel<64, true>, grid, dim3(kThreads), 0, st, a);
+  return a.c.d == 128 ? launch_pdl(q8_mass_rows_kernel<128, false>, grid, dim3(kThreads), 0, st, a)
+                      : launch_pdl(q8_mass_rows_kernel<64, false>, grid, dim3(kThreads), 0, st, a);
 }
 cudaError_t launch_q8_mass_f32(const Q8MassArgs& a, int n_sm, cudaStream_t st) {
-  const dim3 grid(mass_blocks(a.c.cap, kThreads / 8, a.c.H, n_sm, 8), a.c.H);
+  const dim3 grid(mass_blocks(a.c.cap, kThreads / 8 * kF32Keys, a.c.H, n_sm, 4), a.c.H);
   LaunchTrace trace("q8_mass_f32_kernel", st);
-  return a.c.d == 128 ? launch_pdl(q8_mass_f32_kernel<128>, grid, dim3(kThreads), 0, st, a)
-                      : launch_pdl(q8_mass_f32_kernel<64>, grid, dim3(kThreads), 0, st, a);
+  if (a.Nq == 1)
+    return a.c.d == 128 ? launch_pdl(q8_mass_f32_kernel<128, true>, grid, dim3(kThreads), 0, st, a)
+                        : launch_pdl(q8_mass_f32_kernel<64, true>, grid, dim3(kThreads), 0, st, a);
+  return a.c.d == 128 ? launch_pdl(q8_mass_f32_kernel<128, false>, grid, dim3(kThreads), 0, st, a)
+                      : launch_pdl(q8_mass_f32_kernel<64, false>, grid, dim3(kThreads), 0, st, a);
 }
 
 }  // namespace kvb

@@ -124,6 +124,31 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
   __syncthreads();
   const int t0 = blockIdx.x * kTok;
   const int nt = min(kTok, a.n - t0);
+  const T* X = static_cast<const T*>(a.X);
+  T* out = static_cast<T*>(a.out);
+  const int h0 = blockIdx.y * a.heads_per_cta;
+  const int nh = min(a.heads_per_cta, a.heads - h0);
+  const int per = a.d / 8;  // groups per row
+  const int total = nh * nt * per;
+  Raw<T, HALVES> w[kFlight];
+  int pair[kFlight], tok[kFlight];
+  long long to[kFlight];
+  auto load = [&](int base) {
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      const int i = base + u * kThreads;
+      pair[u] = -1;
+      if (i >= total) continue;
+      const int row = i / per, g = i - row * per;
+      const int h = row / nt;
+      tok[u] = row - h * nt;
+      pair[u] = g * 4;
+      const int e = HALVES ? g * 4 : g * 8;
+      w[u].load(X + (h0 + h) * a.xh + (t0 + tok[u]) * a.xt + e, half);
+      to[u] = (h0 + h) * a.oh + (t0 + tok[u]) * a.ot + e;
+    }
+  };
+  load(tid);  // in flight over the angles
   for (int i = tid; i < nt * half; i += kThreads) {
     const int t = i / half, k = i % half;
     float2 v = make_float2(1.f, 0.f);
@@ -142,29 +167,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
     cs[t][k] = v;
   }
   __syncthreads();
-  const T* X = static_cast<const T*>(a.X);
-  T* out = static_cast<T*>(a.out);
-  const int h0 = blockIdx.y * a.heads_per_cta;
-  const int nh = min(a.heads_per_cta, a.heads - h0);
-  const int per = a.d / 8;  // groups per row
-  const int total = nh * nt * per;
   for (int base = tid; base < total; base += kThreads * kFlight) {
-    Raw<T, HALVES> w[kFlight];
-    int pair[kFlight], tok[kFlight];
-    long long to[kFlight];
-#pragma unroll
-    for (int u = 0; u < kFlight; ++u) {
-      const int i = base + u * kThreads;
-      pair[u] = -1;
-      if (i >= total) continue;
-      const int row = i / per, g = i - row * per;
-      const int h = row / nt;
-      tok[u] = row - h * nt;
-      pair[u] = g * 4;
-      const int e = HALVES ? g * 4 : g * 8;
-      w[u].load(X + (h0 + h) * a.xh + (t0 + tok[u]) * a.xt + e, half);
-      to[u] = (h0 + h) * a.oh + (t0 + tok[u]) * a.ot + e;
-    }
+    if (base != tid) load(base);
 #pragma unroll
     for (int u = 0; u < kFlight; ++u) {
       if (pair[u] < 0) continue;
