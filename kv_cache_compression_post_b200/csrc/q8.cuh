@@ -75,6 +75,7 @@ struct Q8Sched {
   int T[kQ8MaxHeads];
   long long total;
   int G;
+  bool small;  // total * G < 2^32: 32-bit quotients do (a 64-bit one takes ~400 clk)
 };
 
 struct Q8Split {
@@ -83,8 +84,15 @@ struct Q8Split {
   int w, wlast;    // cost of a key tile; in the last row tile
   __device__ int wt(int r) const { return r == nrt - 1 ? wlast : w; }
   __device__ long long start(int h, int r) const { return s->C[h] + static_cast<long long>(r) * w * s->T[h]; }
-  __device__ int cta_of(long long x) const { return static_cast<int>((x * s->G) / s->total); }
-  __device__ long long lo(int c) const { return (static_cast<long long>(c) * s->total + s->G - 1) / s->G; }
+  __device__ int cta_of(long long x) const {
+    if (s->small) return static_cast<int>((static_cast<uint32_t>(x) * static_cast<uint32_t>(s->G)) / static_cast<uint32_t>(s->total));
+    return static_cast<int>((x * s->G) / s->total);
+  }
+  __device__ long long lo(int c) const {
+    if (s->small)
+      return (static_cast<uint32_t>(c) * static_cast<uint32_t>(s->total) + static_cast<uint32_t>(s->G - 1)) / static_cast<uint32_t>(s->G);
+    return (static_cast<long long>(c) * s->total + s->G - 1) / s->G;
+  }
 };
 
 // Filled by the whole CTA (blockDim.x a multiple of 32); `min_cost`: a CTA's share is
@@ -113,6 +121,7 @@ __device__ __forceinline__ void q8_build_sched(Q8Sched* s, const int* len, int c
       s->total = carry;
       const long long g = carry / min_cost;
       s->G = static_cast<int>(g < 1 ? 1 : (g < grid ? g : grid));
+      s->small = (carry + 1) * (s->G + 1) < (1ll << 32);
     }
   }
   __syncthreads();
@@ -168,10 +177,12 @@ struct Q8Walk {
     j = 0;
     if (S.s->T[h] > 0) {
       const long long unit = static_cast<long long>(S.w) * S.s->T[h];
-      r = static_cast<int>((x - S.s->C[h]) / unit);
+      r = S.s->small ? static_cast<int>(static_cast<uint32_t>(x - S.s->C[h]) / static_cast<uint32_t>(unit))
+                     : static_cast<int>((x - S.s->C[h]) / unit);
       if (r > S.nrt - 1) r = S.nrt - 1;
       const int w = S.wt(r);
-      j = static_cast<int>((x - S.start(h, r) + w - 1) / w);
+      const long long d = x - S.start(h, r) + w - 1;
+      j = S.s->small ? static_cast<int>(static_cast<uint32_t>(d) / static_cast<uint32_t>(w)) : static_cast<int>(d / w);
     }
     skip_done(S);
   }
@@ -180,7 +191,7 @@ struct Q8Walk {
     const long long cu = S.start(h, r);
     const int w = S.wt(r);
     if (cu + static_cast<long long>(w) * j >= hi) return false;
-    const long long je = (hi - cu + w - 1) / w;
+    const long long je = S.s->small ? static_cast<uint32_t>(hi - cu + w - 1) / static_cast<uint32_t>(w) : (hi - cu + w - 1) / w;
     const int T = S.s->T[h];
     pc.h = h;
     pc.r = r;

@@ -10,17 +10,21 @@
 // m16n8k32 steps, so Q is fetched in that order of channels; it takes 16 contiguous bytes
 // of V for the four tokens its P columns stand for, and output column n of MMA j is
 // channel 16 n + j.
-// K's codes are multiplied as they lie, against two E4M3 parts of each query element
-// (q = hi + lo, exact down to 2^-17 of the row's largest; up to eight rows carry them as
-// the upper and lower half of one 16-row operand).  Widening a pair of codes to fp16
-// takes 8 clk of a scheduler's ALU: with K widened, too, that and not the memory was the
-// bound (8 heads x 8 rows x 98304 tokens on average: 73 us).  V is widened, exactly, and
-// P is fp16.
+// Codes are multiplied as they lie, K's against two E4M3 parts of each query element
+// (q = hi + lo, exact down to 2^-17 of the row's largest), V's, four tokens' bytes of a
+// channel gathered into a word, against two of each weight.  Up to eight rows carry the
+// parts as the upper and lower half of one 16-row operand.  Widening a pair of codes to
+// fp16 takes 8 clk of a scheduler's ALU; with K and V widened that and not the memory was
+// the bound (8 heads, 8 rows, 98304 tokens on average: 73 us, with V alone 56 us).
+//
 // Softmax in the log2 domain.  With ks, vs the scales of a token's block,
-//     x = (q.k) ks scale log2 e,   P = 2^(x + log2 vs - m + kPBias),
-// m the running maximum of x + log2 vs: V's scale rides in the exponent at no cost,
-// P never exceeds 2^kPBias in fp16, and the row sum adds P / vs per block.  Sums,
-// maxima and partial outputs are fp32.
+//     x = (q.k) ks scale log2 e + log2 vs,   P = 2^(x - mt + 7),
+// mt the largest x of the row in the 32 tokens of a step: V's scale rides in the exponent,
+// the row sum adds P / vs per block, and a step's P V enters O by 2^(mt - 7 - m), m the
+// running maximum.  P <= 2^7 in two parts is off by at most 2^-9 of itself (a 4-bit
+// significand, and one of the rest) plus 2^-17 of the step's largest: what bf16 weights
+// would be off by, which the bf16 output's own rounding covers.  Sums, maxima and partial
+// outputs are fp32.
 #include "host_util.h"
 #include "q8.cuh"
 #include "sm100.cuh"
@@ -35,16 +39,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kTile = 64;    // tokens per key tile of the split
 constexpr int kSub = 32;     // tokens a warp takes at a time
 constexpr int kRows = 16;    // rows per row tile
-constexpr float kPBias = 8.f;
+constexpr float kPBias = 7.f;  // log2 of the largest weight of a step
 constexpr int kMinTiles = 4;  // a CTA's share: one 32-token step for each warp
 constexpr int kRing = 3;      // stages of a warp's ring
-
-__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 
 __device__ __forceinline__ float quad_max(float v) {
   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
@@ -225,16 +222,39 @@ struct VWords {
         }
       }
   }
-  // o[j] += P[16 tokens of half u] V, channel (D / 8) n + j in column n
-  __device__ __forceinline__ void accumulate(int u, const uint32_t (&p)[4], float (&o)[D / 8][4]) const {
+  // o[j] += beta P V over the 32 tokens, channel (D / 8) n + j in column n: rows g (0, 1)
+  // and, unless FEW, g + 8 (2, 3).  p: the weights' parts as A operands, like Q's.
+  template <bool FEW>
+  __device__ __forceinline__ void accumulate(const uint32_t (&p)[FEW ? 1 : 2][4], const float (&beta)[FEW ? 1 : 2],
+                                             float (&o)[D / 8][FEW ? 2 : 4]) const {
 #pragma unroll
     for (int q = 0; q < kW; ++q) {
-      const uint32_t a0 = __byte_perm(w[u][0][q], w[u][1][q], 0x5140), a1 = __byte_perm(w[u][0][q], w[u][1][q], 0x7362);
-      const uint32_t b0 = __byte_perm(w[u][2][q], w[u][3][q], 0x5140), b1 = __byte_perm(w[u][2][q], w[u][3][q], 0x7362);
-      mma_16816(o[4 * q + 0], p, e4m3x2_to_f16x2(a0), e4m3x2_to_f16x2(b0));
-      mma_16816(o[4 * q + 1], p, e4m3x2_to_f16x2(a0 >> 16), e4m3x2_to_f16x2(b0 >> 16));
-      mma_16816(o[4 * q + 2], p, e4m3x2_to_f16x2(a1), e4m3x2_to_f16x2(b1));
-      mma_16816(o[4 * q + 3], p, e4m3x2_to_f16x2(a1 >> 16), e4m3x2_to_f16x2(b1 >> 16));
+      uint32_t b[2][4];  // [token half][channel 4 q + i]: that channel's bytes of four tokens
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t x0 = __byte_perm(w[u][0][q], w[u][1][q], 0x5140), x1 = __byte_perm(w[u][2][q], w[u][3][q], 0x5140);
+        const uint32_t x2 = __byte_perm(w[u][0][q], w[u][1][q], 0x7362), x3 = __byte_perm(w[u][2][q], w[u][3][q], 0x7362);
+        b[u][0] = __byte_perm(x0, x1, 0x5410);
+        b[u][1] = __byte_perm(x0, x1, 0x7632);
+        b[u][2] = __byte_perm(x2, x3, 0x5410);
+        b[u][3] = __byte_perm(x2, x3, 0x7632);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+        float(&to)[FEW ? 2 : 4] = o[4 * q + i];
+#pragma unroll
+        for (int part = 0; part < (FEW ? 1 : 2); ++part) mma_16832_e4m3(c, p[part], b[0][i], b[1][i]);
+        if constexpr (FEW) {
+          to[0] = fmaf(beta[0], c[0] + c[2], to[0]);
+          to[1] = fmaf(beta[0], c[1] + c[3], to[1]);
+        } else {
+          to[0] = fmaf(beta[0], c[0], to[0]);
+          to[1] = fmaf(beta[0], c[1], to[1]);
+          to[2] = fmaf(beta[1], c[2], to[2]);
+          to[3] = fmaf(beta[1], c[3], to[3]);
+        }
+      }
     }
   }
 };
@@ -297,11 +317,11 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_rows_kernel(const Q8Att
     scales(first);
     QFrag<D, FEW> q;
     q.load(static_cast<const __nv_bfloat16*>(a.Q) + row0 * D, rows, a.scale, g, t);
-    float o[D / 8][4];
+    float o[D / 8][2 * kI];
 #pragma unroll
     for (int j = 0; j < D / 8; ++j)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) o[j][k] = 0.f;
+      for (int k = 0; k < 2 * kI; ++k) o[j][k] = 0.f;
     float m[kI], l[kI];
 #pragma unroll
     for (int i = 0; i < kI; ++i) m[i] = -INFINITY, l[i] = 0.f;
@@ -362,24 +382,37 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_rows_kernel(const Q8Att
       VWords<D> vw;
       vw.load(ring + stage * kStage + 32 * D, g, t);
       stage = stage == kRing - 1 ? 0 : stage + 1;
+      // weights of the lane's eight tokens, four to a word: those of 16-token half u
+      uint32_t p[kI][4];
+      float beta[kI];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        uint32_t p[4] = {0u, 0u, 0u, 0u};
+      for (int i = 0; i < kI; ++i) {
+        beta[i] = ex2_approx(mt[i] - m[i] - kPBias);
+        const float b = kPBias - mt[i];
+        float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < kI; ++i) {
-          // a row whose every score is -inf so far (NaN queries aside) keeps P = 0
-          const float b = (m[i] == -INFINITY ? 0.f : -m[i]) + kPBias;
-          float r = 0.f;
+        for (int u = 0; u < 2; ++u) {
+          float e[4], r = 0.f;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float x = ex2_approx(s[2 * u + j][2 * i] + b), y = ex2_approx(s[2 * u + j][2 * i + 1] + b);
-            r += x + y;
-            p[2 * j + i] = pack_f16x2(x, y);
+          for (int k = 0; k < 4; ++k) {
+            e[k] = ex2_approx(s[2 * u + (k >> 1)][2 * i + (k & 1)] + b);
+            r += e[k];
           }
-          l[i] = fmaf(r, iv[u], l[i]);
+          sum = fmaf(r, iv[u], sum);
+          const uint32_t c0 = f32x2_to_e4m3x2(e[0], e[1]), c1 = f32x2_to_e4m3x2(e[2], e[3]);
+          const float2 h0 = e4m3x2_to_f32x2(c0), h1 = e4m3x2_to_f32x2(c1);
+          const uint32_t lo = f32x2_to_e4m3x2(e[0] - h0.x, e[1] - h0.y) | (f32x2_to_e4m3x2(e[2] - h1.x, e[3] - h1.y) << 16);
+          if constexpr (FEW) {
+            p[0][2 * u] = c0 | (c1 << 16);
+            p[0][2 * u + 1] = lo;
+          } else {
+            p[0][i + 2 * u] = c0 | (c1 << 16);
+            p[1][i + 2 * u] = lo;
+          }
         }
-        vw.accumulate(u, p, o);
+        l[i] = fmaf(sum, beta[i], l[i]);
       }
+      vw.template accumulate<FEW>(p, beta, o);
     }
     // merge the eight warps: maxima first, then every output weighted by its warp
 #pragma unroll
@@ -422,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_rows_kernel(const Q8Att
         const float inv = 1.f / L;
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + (row0 + row) * D + c) =
             make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-        if (a.lse && c == 0) a.lse[row0 + row] = (M - kPBias + log2f(L)) * kLn2;
+        if (a.lse && c == 0) a.lse[row0 + row] = (M + log2f(L)) * kLn2;
       } else {
         *reinterpret_cast<float4*>(slot + row * D + c) = acc;
         if (c == 0) {
@@ -442,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_rows_kernel(const Q8Att
 constexpr int kMergeThreads = 256;
 template <int D, typename T>
 __global__ void __launch_bounds__(kMergeThreads) q8_merge_rows_kernel(const Q8AttendArgs a, int tile_rows, int tile,
-                                                                      int grid, int min_tiles, float bias) {
+                                                                      int grid, int min_tiles) {
   __shared__ Q8Sched sch;
   __shared__ float s_w[kRows][kQ8MaxCtas], s_l[kRows][kQ8MaxCtas];
   pdl_wait();
@@ -494,7 +527,7 @@ __global__ void __launch_bounds__(kMergeThreads) q8_merge_rows_kernel(const Q8At
     L = warp_sum(L);
     if (lane == 0) {
       s_l[row][0] = 1.f / L;
-      if (a.lse) a.lse[row0 + row] = (M - bias + log2f(L)) * kLn2;
+      if (a.lse) a.lse[row0 + row] = (M + log2f(L)) * kLn2;
     }
   }
   __syncthreads();
@@ -785,7 +818,7 @@ cudaError_t attend_rows(const Q8AttendArgs& a, int n_sm, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   LaunchTrace trace("q8_merge_rows_kernel", st);
   return launch_pdl(q8_merge_rows_kernel<D, __nv_bfloat16>, dim3((a.Nq + kRows - 1) / kRows, a.c.H), dim3(kMergeThreads), 0, st, a,
-                    static_cast<int>(kRows), static_cast<int>(kTile), grid, static_cast<int>(kMinTiles), static_cast<float>(kPBias));
+                    static_cast<int>(kRows), static_cast<int>(kTile), grid, static_cast<int>(kMinTiles));
 }
 
 template <int D>
@@ -800,7 +833,7 @@ cudaError_t attend_f32(const Q8AttendArgs& a, int n_sm, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   LaunchTrace trace("q8_merge_rows_kernel", st);
   return launch_pdl(q8_merge_rows_kernel<D, float>, dim3((a.Nq + kF32Rows - 1) / kF32Rows, a.c.H), dim3(kMergeThreads), 0, st, a,
-                    static_cast<int>(kF32Rows), static_cast<int>(kTile), grid, static_cast<int>(kMinTiles), 0.f);
+                    static_cast<int>(kF32Rows), static_cast<int>(kTile), grid, static_cast<int>(kMinTiles));
 }
 
 // CTAs per head so that the grid is about `waves` waves, no more than the tokens need

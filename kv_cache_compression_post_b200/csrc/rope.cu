@@ -6,7 +6,8 @@
 // applies them to the rows of every head of its share.  Far positions lose their angle
 // in fp32 (position 1e6 has steps of 0.06 rad), so angles are formed and reduced to
 // [-pi, pi] in fp64; the remainder is split into two floats, sine and cosine taken of
-// the first and corrected by the second: cos(h + l) = cos h - l sin h, error ~1 ulp.
+// the first (in half turns) and corrected by the second: cos(h + l) = cos h - l sin h,
+// error ~1 ulp.
 // Bound by memory: one read and one write of every element.  A thread moves four
 // pairs (16 bytes of bf16, interleaved), four such groups in flight.
 #include <cuda_bf16.h>
@@ -19,10 +20,9 @@
 namespace kvb {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kTok = 8;         // tokens per CTA
+constexpr int kThreads = 128;
+constexpr int kTok = 4;         // tokens per CTA
 constexpr int kMaxPairs = 128;  // head_dim <= 256
-constexpr int kFlight = 4;      // groups of four pairs in flight per thread
 
 struct RopeArgs {
   const void* X;
@@ -109,6 +109,7 @@ struct Raw<float, HALVES> {
 
 template <typename T, bool HALVES>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
+  constexpr int kFlight = sizeof(T) == 2 ? 4 : 2;  // groups of four pairs in flight per thread: 64 bytes
   __shared__ double freq[kMaxPairs];
   __shared__ float2 cs[kTok][kMaxPairs];
   const int half = a.d / 2;
@@ -158,9 +159,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
       // x - n 2 pi, 2 pi as two doubles
       const double n = rint(x * 0.15915494309189535);
       const double r = fma(-n, 2.4492935982947064e-16, fma(-n, 6.283185307179586, x));
-      const float h = static_cast<float>(r), l = static_cast<float>(r - static_cast<double>(h));
+      const double turn = r * 0.3183098861837907;  // in half turns, |turn| <= 1
+      const float h = static_cast<float>(turn);
+      const float l = static_cast<float>((turn - static_cast<double>(h)) * 3.141592653589793);
       float s, c;
-      sincosf(h, &s, &c);
+      sincospif(h, &s, &c);
       v = make_float2(fmaf(-l, s, c), fmaf(l, c, s));
       if (a.inverse) v.y = -v.y;
     }
