@@ -1,5 +1,6 @@
 // C entry points of the 8-bit block-scaled cache: argument checks, workspace layout
 // and the choice of kernel.
+#include <atomic>
 #include <cmath>
 
 #include "host_util.h"
@@ -33,9 +34,11 @@ Q8View view(const kvb_q8_cache* c) {
 
 bool dtype_ok(kvb_dtype t) { return t == KVB_BF16 || t == KVB_F32; }
 
-// One scratch serves every call on a cache: partials of the row-tile kernels, the
-// positions an eviction keeps, or what a chunk of queries needs, each from its start.
+// One scratch serves every call on a cache: the row-tile kernels' arrival counters, which
+// nothing else may write, then their partials, the positions an eviction keeps, or what a
+// chunk of queries needs, each from there.
 struct Scratch {
+  unsigned long long* cnt = nullptr;
   float* part = nullptr;
   int* kept = nullptr;
   Q8ChunkScratch chunk{};
@@ -47,13 +50,13 @@ bool chunk_kernel(int32_t rows, kvb_dtype dtype) { return dtype == KVB_BF16 && r
 Scratch scratch(const kvb_q8_cache* c, int32_t max_queries, kvb_dtype dtype, void* ws) {
   Scratch s;
   Carver a(ws);
+  s.cnt = a.take<unsigned long long>(kQ8RowCounters);
+  Carver e = a, q = a;
   s.part = a.take<float>(q8_part_floats(c->head_dim));
-  Carver e(ws);
   s.kept = e.take<int>(static_cast<size_t>(c->heads) * c->capacity);
   s.bytes = a.bytes() > e.bytes() ? a.bytes() : e.bytes();
   if (chunk_kernel(max_queries, dtype)) {
     const size_t rows = static_cast<size_t>(c->heads) * max_queries;
-    Carver q(ws);
     s.chunk.hi = q.take<uint8_t>(rows * c->head_dim);
     s.chunk.lo = q.take<uint8_t>(rows * c->head_dim);
     s.chunk.coef = q.take<float>(rows);
@@ -130,6 +133,10 @@ kvb_status kvb_q8_attend(const kvb_q8_cache* c, const void* Q, int32_t Nq, kvb_d
   a.O = O;
   a.lse = lse;
   a.part = s.part;
+  a.cnt = s.cnt;
+  static std::atomic<unsigned int> calls{0};
+  do a.epoch = calls.fetch_add(1, std::memory_order_relaxed) + 1;
+  while (a.epoch == 0);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == KVB_F32) return cuda_status(launch_q8_attend_f32(a, dev.n_sm, st));
   if (chunk_kernel(Nq, dtype)) return cuda_status(launch_q8_attend_chunk(a, s.chunk, dev.n_sm, st));

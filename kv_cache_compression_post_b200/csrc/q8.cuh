@@ -186,7 +186,8 @@ struct Q8Walk {
     }
     skip_done(S);
   }
-  __device__ bool next(const Q8Split& S, Q8Piece& pc) {
+  // whole: with the unit's pieces (a caller in a hurry finds them later, q8_unit_pieces)
+  __device__ bool next(const Q8Split& S, Q8Piece& pc, bool whole = true) {
     if (h >= S.H) return false;
     const long long cu = S.start(h, r);
     const int w = S.wt(r);
@@ -197,7 +198,7 @@ struct Q8Walk {
     pc.r = r;
     pc.j0 = j;
     pc.j1 = je < T ? static_cast<int>(je) : T;
-    q8_unit_pieces(S, h, r, pc);
+    if (whole) q8_unit_pieces(S, h, r, pc);
     pc.which = first ? 0 : 1;
     first = false;
     j = pc.j1;
@@ -215,6 +216,8 @@ struct Q8AttendArgs {
   void* O;
   float* lse;
   float* part;  // partials: q8_part_floats(d) floats
+  unsigned long long* cnt;  // the row-tile kernels' arrival counters: kQ8RowCounters
+  unsigned int epoch;       // of this launch, nonzero
 };
 
 struct Q8MassArgs {
@@ -233,6 +236,7 @@ cudaError_t launch_q8_attend_f32(const Q8AttendArgs& a, int n_sm, cudaStream_t s
 cudaError_t launch_q8_mass_rows(const Q8MassArgs& a, int n_sm, cudaStream_t st);
 cudaError_t launch_q8_mass_f32(const Q8MassArgs& a, int n_sm, cudaStream_t st);
 
+constexpr int kQ8RowCounters = kQ8MaxCtas * 2;
 // floats of partials the row-tile kernels need: two slots per CTA of 16 rows and
 // their maxima and sums
 inline size_t q8_part_floats(int d) { return static_cast<size_t>(kQ8MaxCtas) * 2 * (16 * d + 32); }

@@ -4,27 +4,25 @@
 // Reading the cache once is the bound (2 bytes per token and channel), so the work is
 // split over its tokens (Q8Split) and every warp streams 32 tokens at a time through a
 // ring of its own in shared memory (cp.async, no barrier between warps) into the
-// fragments of mma.sync.  What the layout relies on: a contraction may run over the
-// channels, and over the tokens, in any order that both operands share.  Lane (g, t) =
-// (lane / 4, lane % 4) takes 16 contiguous bytes of token g's K row and uses them as two
-// m16n8k32 steps, so Q is fetched in that order of channels; it takes 16 contiguous bytes
-// of V for the four tokens its P columns stand for, and output column n of MMA j is
-// channel 16 n + j.
-// Codes are multiplied as they lie, K's against two E4M3 parts of each query element
-// (q = hi + lo, exact down to 2^-17 of the row's largest), V's, four tokens' bytes of a
-// channel gathered into a word, against two of each weight.  Up to eight rows carry the
-// parts as the upper and lower half of one 16-row operand.  Widening a pair of codes to
-// fp16 takes 8 clk of a scheduler's ALU; with K and V widened that and not the memory was
-// the bound (8 heads, 8 rows, 98304 tokens on average: 73 us, with V alone 56 us).
+// fragments of mma.sync.m16n8k16 (16 rows x 8 tokens).  What the layout relies on: a
+// contraction may run over the channels, and over the tokens, in any order that both
+// operands share.  Lane (g, t) = (lane / 4, lane % 4) takes 16 contiguous bytes of token
+// g's K row and uses them as four MMA steps, so Q is fetched in that order of channels;
+// it takes 16 contiguous bytes of V for the four tokens its P columns stand for, and
+// output column n of MMA j is channel 16 n + j.  Codes widen to fp16 exactly, two per
+// instruction, and Q enters as fp16 times a power of two per row (bf16 has 8 bits,
+// fp16 11, so nothing is lost above 2^-14 of the row's largest).
+// What bounds it: widening a pair of codes takes 8 clk of a scheduler's ALU, ~1000 of the
+// ~1500 clk of a 32-token step, beside which the memory would need ~1400 (8 heads, 8 rows,
+// 98304 tokens on average: 41 us of memory alone, 40 us of arithmetic alone, 50 us
+// together, and the merge).  E4M3 operands of mma.sync do not help, they are widened in
+// the same way (same time, measured).
 //
 // Softmax in the log2 domain.  With ks, vs the scales of a token's block,
-//     x = (q.k) ks scale log2 e + log2 vs,   P = 2^(x - mt + 7),
-// mt the largest x of the row in the 32 tokens of a step: V's scale rides in the exponent,
-// the row sum adds P / vs per block, and a step's P V enters O by 2^(mt - 7 - m), m the
-// running maximum.  P <= 2^7 in two parts is off by at most 2^-9 of itself (a 4-bit
-// significand, and one of the rest) plus 2^-17 of the step's largest: what bf16 weights
-// would be off by, which the bf16 output's own rounding covers.  Sums, maxima and partial
-// outputs are fp32.
+//     x = (q.k) ks scale log2 e,   P = 2^(x + log2 vs - m + kPBias),
+// m the running maximum of x + log2 vs: V's scale rides in the exponent at no cost,
+// P never exceeds 2^kPBias in fp16, and the row sum adds P / vs per block.  Sums,
+// maxima and partial outputs are fp32.
 #include "host_util.h"
 #include "q8.cuh"
 #include "sm100.cuh"
@@ -35,13 +33,20 @@ using namespace sm100;
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kWarps = kThreads / 32;  // ten or twelve warps, with their registers cut to fit, were slower
+constexpr int kRing = 2;               // stages of a warp's ring (three: 5 % slower)
 constexpr int kTile = 64;    // tokens per key tile of the split
 constexpr int kSub = 32;     // tokens a warp takes at a time
 constexpr int kRows = 16;    // rows per row tile
-constexpr float kPBias = 7.f;  // log2 of the largest weight of a step
+constexpr float kPBias = 8.f;
 constexpr int kMinTiles = 4;  // a CTA's share: one 32-token step for each warp
-constexpr int kRing = 3;      // stages of a warp's ring
+
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 
 __device__ __forceinline__ float quad_max(float v) {
   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
@@ -52,35 +57,32 @@ __device__ __forceinline__ float quad_sum(float v) {
   return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
 
-__device__ __forceinline__ void mma_16832_e4m3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// The A fragments of one row tile: the two E4M3 parts of rows g (and g + 8), channels
-// 64 hb + 16 t .. + 15 in the order the K bytes come.  FEW (at most eight rows): the
-// lower half of the operand holds the second parts; otherwise they are an operand of
-// their own.  coef[i]: what turns a raw dot product of row g + 8 i into log2 units (but
-// for the token's scale).
+// The A fragments of one 16-row tile: row g and, unless FEW (at most eight rows), g + 8 of
+// this lane, channels 64 hb + 16 t .. + 15 in the order the K bytes come.  coef[i]: what
+// turns a raw dot product of row g + 8 i into log2 units (but for the token's scale).
 template <int D, bool FEW>
 struct QFrag {
   static constexpr int kI = FEW ? 1 : 2;
-  uint32_t a[D / 32][FEW ? 1 : 2][4];  // [32-channel step][part][register]
+  uint32_t a[D / 16][2 * kI];  // [16-channel step][(half of the step) * kI + row]
   float coef[kI];
+  uint4 raw[kI][D / 32];
 
-  __device__ __forceinline__ void load(const __nv_bfloat16* Q, int rows, float scale, int g, int t) {
+  __device__ __forceinline__ void fetch(const __nv_bfloat16* Q, int rows, int g, int t) {
 #pragma unroll
     for (int i = 0; i < kI; ++i) {
       const int row = g + 8 * i;
-      uint4 w[D / 32];
 #pragma unroll
       for (int hb = 0; hb < D / 64; ++hb)
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-          w[hb * 2 + k] = row < rows ? *(reinterpret_cast<const uint4*>(Q + static_cast<size_t>(row) * D + hb * 64 + t * 16) + k)
-                                     : make_uint4(0u, 0u, 0u, 0u);
+          raw[i][hb * 2 + k] = row < rows ? *(reinterpret_cast<const uint4*>(Q + static_cast<size_t>(row) * D + hb * 64 + t * 16) + k)
+                                          : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  __device__ __forceinline__ void widen(float scale) {
+#pragma unroll
+    for (int i = 0; i < kI; ++i) {
+      const uint4(&w)[D / 32] = raw[i];
       float mx = 0.f;
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) {
@@ -93,36 +95,24 @@ struct QFrag {
         }
       }
       mx = quad_max(mx);
-      const int e = max(exponent_of(mx), -100) - 7;  // mx 2^-e in [2^7, 2^8)
+      const int e = min(max(exponent_of(mx), -100), 126);
       const float down = pow2f(-e);
       coef[i] = pow2f(e) * scale * kLog2e;
-      // eight channels: one step; its first four to register i, the others to i + 2
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) {
+        // 8 channels: two MMA steps, (0,1) and (2,3) of each to their two halves
         const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t hi = 0u, lo = 0u;
-#pragma unroll
-          for (int e2 = 0; e2 < 2; ++e2) {
-            const float2 f = unpack_bf16x2(u[half * 2 + e2]);
-            // an infinite element becomes a NaN: its row is NaN, as its scores would be
-            const float x = fabsf(f.x) <= 3.4e38f ? f.x * down : NAN, y = fabsf(f.y) <= 3.4e38f ? f.y * down : NAN;
-            const uint32_t c = f32x2_to_e4m3x2(x, y);
-            const float2 b = e4m3x2_to_f32x2(c);
-            hi |= c << (16 * e2);
-            lo |= f32x2_to_e4m3x2(x - b.x, y - b.y) << (16 * e2);
-          }
-          if constexpr (FEW) {
-            a[k][0][2 * half] = hi;
-            a[k][0][2 * half + 1] = lo;
-          } else {
-            a[k][0][i + 2 * half] = hi;
-            a[k][1][i + 2 * half] = lo;
-          }
+        for (int e2 = 0; e2 < 4; ++e2) {
+          const float2 f = unpack_bf16x2(u[e2]);
+          a[k * 2 + (e2 >> 1)][i + kI * (e2 & 1)] = pack_f16x2(f.x * down, f.y * down);
         }
       }
     }
+  }
+  __device__ __forceinline__ void step(float (&c)[4], int k, uint32_t b0, uint32_t b1) const {
+    const uint32_t r[4] = {a[k][0], FEW ? 0u : a[k][1], a[k][kI], FEW ? 0u : a[k][2 * kI - 1]};
+    mma_16816(c, r, b0, b1);
   }
 };
 
@@ -189,14 +179,7 @@ struct KWords {
       for (int hb = 0; hb < D / 64; ++hb) {
         const uint32_t u[4] = {w[j][hb].x, w[j][hb].y, w[j][hb].z, w[j][hb].w};
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int part = 0; part < (FEW ? 1 : 2); ++part)
-            mma_16832_e4m3(s[j], q.a[hb * 2 + i][part], u[2 * i], u[2 * i + 1]);
-      }
-      if constexpr (FEW) {
-        s[j][0] += s[j][2];
-        s[j][1] += s[j][3];
+        for (int i = 0; i < 4; ++i) q.step(s[j], hb * 4 + i, e4m3x2_to_f16x2(u[i]), e4m3x2_to_f16x2(u[i] >> 16));
       }
     }
   }
@@ -222,39 +205,16 @@ struct VWords {
         }
       }
   }
-  // o[j] += beta P V over the 32 tokens, channel (D / 8) n + j in column n: rows g (0, 1)
-  // and, unless FEW, g + 8 (2, 3).  p: the weights' parts as A operands, like Q's.
-  template <bool FEW>
-  __device__ __forceinline__ void accumulate(const uint32_t (&p)[FEW ? 1 : 2][4], const float (&beta)[FEW ? 1 : 2],
-                                             float (&o)[D / 8][FEW ? 2 : 4]) const {
+  // o[j] += P[16 tokens of half u] V, channel (D / 8) n + j in column n
+  __device__ __forceinline__ void accumulate(int u, const uint32_t (&p)[4], float (&o)[D / 8][4]) const {
 #pragma unroll
     for (int q = 0; q < kW; ++q) {
-      uint32_t b[2][4];  // [token half][channel 4 q + i]: that channel's bytes of four tokens
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint32_t x0 = __byte_perm(w[u][0][q], w[u][1][q], 0x5140), x1 = __byte_perm(w[u][2][q], w[u][3][q], 0x5140);
-        const uint32_t x2 = __byte_perm(w[u][0][q], w[u][1][q], 0x7362), x3 = __byte_perm(w[u][2][q], w[u][3][q], 0x7362);
-        b[u][0] = __byte_perm(x0, x1, 0x5410);
-        b[u][1] = __byte_perm(x0, x1, 0x7632);
-        b[u][2] = __byte_perm(x2, x3, 0x5410);
-        b[u][3] = __byte_perm(x2, x3, 0x7632);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
-        float(&to)[FEW ? 2 : 4] = o[4 * q + i];
-#pragma unroll
-        for (int part = 0; part < (FEW ? 1 : 2); ++part) mma_16832_e4m3(c, p[part], b[0][i], b[1][i]);
-        if constexpr (FEW) {
-          to[0] = fmaf(beta[0], c[0] + c[2], to[0]);
-          to[1] = fmaf(beta[0], c[1] + c[3], to[1]);
-        } else {
-          to[0] = fmaf(beta[0], c[0], to[0]);
-          to[1] = fmaf(beta[0], c[1], to[1]);
-          to[2] = fmaf(beta[1], c[2], to[2]);
-          to[3] = fmaf(beta[1], c[3], to[3]);
-        }
-      }
+      const uint32_t a0 = __byte_perm(w[u][0][q], w[u][1][q], 0x5140), a1 = __byte_perm(w[u][0][q], w[u][1][q], 0x7362);
+      const uint32_t b0 = __byte_perm(w[u][2][q], w[u][3][q], 0x5140), b1 = __byte_perm(w[u][2][q], w[u][3][q], 0x7362);
+      mma_16816(o[4 * q + 0], p, e4m3x2_to_f16x2(a0), e4m3x2_to_f16x2(b0));
+      mma_16816(o[4 * q + 1], p, e4m3x2_to_f16x2(a0 >> 16), e4m3x2_to_f16x2(b0 >> 16));
+      mma_16816(o[4 * q + 2], p, e4m3x2_to_f16x2(a1), e4m3x2_to_f16x2(b1));
+      mma_16816(o[4 * q + 3], p, e4m3x2_to_f16x2(a1 >> 16), e4m3x2_to_f16x2(b1 >> 16));
     }
   }
 };
@@ -269,11 +229,121 @@ struct RowsShared {
   float m[kWarps][kRows], l[kWarps][kRows];
 };
 
+// Arrival at a cut unit's counter: true for the last of its pieces, which resets it.  The
+// count is tagged with the launch's epoch, so the counters need no initialisation; a
+// replayed launch finds them reset by its earlier run.
+__device__ __forceinline__ bool arrive_last(unsigned long long* cp, unsigned int epoch, int npieces) {
+  unsigned long long cur = *reinterpret_cast<volatile unsigned long long*>(cp);
+  for (;;) {  // every failed exchange is another piece's success: at most npieces rounds
+    const unsigned int have = static_cast<unsigned int>(cur >> 32) == epoch ? static_cast<unsigned int>(cur) : 0u;
+    const bool fin = have + 1 >= static_cast<unsigned int>(npieces);
+    const unsigned long long want = fin ? 0ull : (static_cast<unsigned long long>(epoch) << 32) | (have + 1);
+    const unsigned long long was = atomicCAS(cp, cur, want);
+    if (was == cur) return fin;
+    cur = was;
+  }
+}
+
+template <typename T, int D>
+__device__ __forceinline__ void put_row4(void* O, size_t row, int c, float4 v) {
+  T* p = static_cast<T*>(O) + row * D + c;
+  if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+  else *reinterpret_cast<float4*>(p) = v;
+}
+
+// The last piece of a unit to arrive merges them all, in their order: the pieces' maxima
+// and sums, fetched at once, become one weight per (row, piece); then the outputs, with
+// eight fetches in flight.  (A second kernel for it cost 6 us.)  Called by the whole CTA
+// after it has stored its own piece; s_w, s_l: shared memory, ROWS x kQ8MaxCtas each.
+template <int D, typename T, int ROWS>
+__device__ void finish_unit(const Q8AttendArgs& a, const Q8Piece& pc, size_t row0, int rows, float bias, float* s_w,
+                            float* s_l, int* s_last) {
+  const int tid = threadIdx.x, nthreads = blockDim.x, np = pc.npieces;
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) *s_last = arrive_last(a.cnt + pc.cfirst * 2 + pc.wfirst, a.epoch, np) ? 1 : 0;
+  __syncthreads();
+  if (!*s_last) return;
+  __threadfence();
+  const float* first = a.part + static_cast<size_t>(pc.cfirst * 2 + pc.wfirst) * slot_floats<D>();
+  const float* rest = a.part + static_cast<size_t>(pc.cfirst) * 2 * slot_floats<D>();  // piece k > 0: slot 0 of CTA cfirst + k
+  auto slot = [&](int k) { return k == 0 ? first : rest + static_cast<size_t>(k) * 2 * slot_floats<D>(); };
+  for (int i = tid; i < rows * np; i += nthreads) {
+    const int row = i / np, k = i - row * np;
+    s_w[row * kQ8MaxCtas + k] = __ldcg(slot(k) + kRows * D + row);
+    s_l[row * kQ8MaxCtas + k] = __ldcg(slot(k) + kRows * D + kRows + row);
+  }
+  __syncthreads();
+  const int warp = tid >> 5, lane = tid & 31;
+  for (int row = warp; row < rows; row += nthreads / 32) {
+    float* w = s_w + row * kQ8MaxCtas;
+    float* l = s_l + row * kQ8MaxCtas;
+    float M = -INFINITY;
+    for (int k = lane; k < np; k += 32) M = fmaxf(M, w[k]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float L = 0.f;
+    for (int k = lane; k < np; k += 32) {
+      const float f = M == -INFINITY ? 1.f : exp2f(w[k] - M);
+      w[k] = f;
+      L = fmaf(f, l[k], L);
+    }
+    L = warp_sum(L);
+    __syncwarp();
+    if (lane == 0) {
+      l[0] = 1.f / L;
+      if (a.lse) a.lse[row0 + row] = (M - bias + log2f(L)) * kLn2;
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < rows * (D / 4); i += nthreads) {
+    const int row = i / (D / 4), c = (i % (D / 4)) * 4;
+    const float* w = s_w + row * kQ8MaxCtas;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < np; k0 += 8) {
+      float4 x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (k0 + u < np) x[u] = __ldcg(reinterpret_cast<const float4*>(slot(k0 + u) + row * D + c));
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (k0 + u >= np) continue;
+        const float f = w[k0 + u];
+        acc.x = fmaf(f, x[u].x, acc.x);
+        acc.y = fmaf(f, x[u].y, acc.y);
+        acc.z = fmaf(f, x[u].z, acc.z);
+        acc.w = fmaf(f, x[u].w, acc.w);
+      }
+    }
+    const float inv = s_l[row * kQ8MaxCtas];
+    put_row4<T, D>(a.O, row0 + row, c, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+  }
+}
+
+// rows of heads without tokens: zeros (lse -inf), spread over the CTAs with work (or all
+// left to CTA 0)
+template <int D, typename T>
+__device__ void empty_rows(const Q8AttendArgs& a, const Q8Sched& sch, int tile_rows, int nrt) {
+  for (int h = 0; h < a.c.H; ++h) {
+    if (sch.T[h] != 0) continue;
+    for (int r = 0; r < nrt; ++r) {
+      if ((h * nrt + r) % sch.G != static_cast<int>(blockIdx.x)) continue;
+      const int rows = min(tile_rows, a.Nq - r * tile_rows);
+      const size_t row0 = static_cast<size_t>(h) * a.Nq + r * tile_rows;
+      for (int i = threadIdx.x; i < rows * (D / 4); i += blockDim.x)
+        put_row4<T, D>(a.O, row0 + i / (D / 4), (i % (D / 4)) * 4, make_float4(0.f, 0.f, 0.f, 0.f));
+      if (a.lse)
+        for (int i = threadIdx.x; i < rows; i += blockDim.x) a.lse[row0 + i] = -INFINITY;
+    }
+  }
+}
+
 template <int D, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1) q8_attend_rows_kernel(const Q8AttendArgs a) {
   constexpr int kI = FEW ? 1 : 2;  // rows of a lane: g, g + 8
-  extern __shared__ uint8_t smem[];
+  extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Q8Sched sch;
+  __shared__ int s_last;
   RowsShared<D>& sh = *reinterpret_cast<RowsShared<D>*>(smem);  // over the rings, once they are done with
   pdl_wait();
   pdl_trigger();
@@ -288,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_rows_kernel(const Q8Att
   Q8Walk walk;
   walk.init(S, blockIdx.x);
   Q8Piece pc;
-  while (walk.next(S, pc)) {
+  while (walk.next(S, pc, false)) {
     const int n = q8_len(a.c.len, pc.h, a.c.cap);
     const int end = min(pc.j1 * kTile, n);
     const int rows = min(kRows, a.Nq - pc.r * kRows);
@@ -297,6 +367,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_rows_kernel(const Q8Att
     const uint8_t* V = a.c.V + static_cast<size_t>(pc.h) * a.c.cap * D;
     const float* ks = a.c.ks + static_cast<size_t>(pc.h) * blocks;
     const float* vs = a.c.vs + static_cast<size_t>(pc.h) * blocks;
+    QFrag<D, FEW> q;
+    q.fetch(static_cast<const __nv_bfloat16*>(a.Q) + row0 * D, rows, g, t);
     constexpr int kHop = kWarps * kSub;
     const int first = pc.j0 * kTile + warp * kSub;
 #pragma unroll
@@ -315,13 +387,13 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_rows_kernel(const Q8Att
       }
     };
     scales(first);
-    QFrag<D, FEW> q;
-    q.load(static_cast<const __nv_bfloat16*>(a.Q) + row0 * D, rows, a.scale, g, t);
-    float o[D / 8][2 * kI];
+    q8_unit_pieces(S, pc.h, pc.r, pc);
+    q.widen(a.scale);
+    float o[D / 8][4];  // FEW: rows g + 8 stay 0
 #pragma unroll
     for (int j = 0; j < D / 8; ++j)
 #pragma unroll
-      for (int k = 0; k < 2 * kI; ++k) o[j][k] = 0.f;
+      for (int k = 0; k < 4; ++k) o[j][k] = 0.f;
     float m[kI], l[kI];
 #pragma unroll
     for (int i = 0; i < kI; ++i) m[i] = -INFINITY, l[i] = 0.f;
@@ -382,37 +454,24 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_rows_kernel(const Q8Att
       VWords<D> vw;
       vw.load(ring + stage * kStage + 32 * D, g, t);
       stage = stage == kRing - 1 ? 0 : stage + 1;
-      // weights of the lane's eight tokens, four to a word: those of 16-token half u
-      uint32_t p[kI][4];
-      float beta[kI];
 #pragma unroll
-      for (int i = 0; i < kI; ++i) {
-        beta[i] = ex2_approx(mt[i] - m[i] - kPBias);
-        const float b = kPBias - mt[i];
-        float sum = 0.f;
+      for (int u = 0; u < 2; ++u) {
+        uint32_t p[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          float e[4], r = 0.f;
+        for (int i = 0; i < kI; ++i) {
+          // a row whose every score is -inf so far (NaN queries aside) keeps P = 0
+          const float b = (m[i] == -INFINITY ? 0.f : -m[i]) + kPBias;
+          float r = 0.f;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            e[k] = ex2_approx(s[2 * u + (k >> 1)][2 * i + (k & 1)] + b);
-            r += e[k];
+          for (int j = 0; j < 2; ++j) {
+            const float x = ex2_approx(s[2 * u + j][2 * i] + b), y = ex2_approx(s[2 * u + j][2 * i + 1] + b);
+            r += x + y;
+            p[2 * j + i] = pack_f16x2(x, y);
           }
-          sum = fmaf(r, iv[u], sum);
-          const uint32_t c0 = f32x2_to_e4m3x2(e[0], e[1]), c1 = f32x2_to_e4m3x2(e[2], e[3]);
-          const float2 h0 = e4m3x2_to_f32x2(c0), h1 = e4m3x2_to_f32x2(c1);
-          const uint32_t lo = f32x2_to_e4m3x2(e[0] - h0.x, e[1] - h0.y) | (f32x2_to_e4m3x2(e[2] - h1.x, e[3] - h1.y) << 16);
-          if constexpr (FEW) {
-            p[0][2 * u] = c0 | (c1 << 16);
-            p[0][2 * u + 1] = lo;
-          } else {
-            p[0][i + 2 * u] = c0 | (c1 << 16);
-            p[1][i + 2 * u] = lo;
-          }
+          l[i] = fmaf(r, iv[u], l[i]);
         }
-        l[i] = fmaf(sum, beta[i], l[i]);
+        vw.accumulate(u, p, o);
       }
-      vw.template accumulate<FEW>(p, beta, o);
     }
     // merge the eight warps: maxima first, then every output weighted by its warp
 #pragma unroll
@@ -455,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_rows_kernel(const Q8Att
         const float inv = 1.f / L;
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + (row0 + row) * D + c) =
             make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-        if (a.lse && c == 0) a.lse[row0 + row] = (M + log2f(L)) * kLn2;
+        if (a.lse && c == 0) a.lse[row0 + row] = (M - kPBias + log2f(L)) * kLn2;
       } else {
         *reinterpret_cast<float4*>(slot + row * D + c) = acc;
         if (c == 0) {
@@ -464,94 +523,14 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_rows_kernel(const Q8Att
         }
       }
     }
+    if (pc.npieces > 1) {
+      __syncthreads();  // the warps' outputs have been read
+      float* s_w = reinterpret_cast<float*>(smem);
+      finish_unit<D, __nv_bfloat16, kRows>(a, pc, row0, rows, kPBias, s_w, s_w + kRows * kQ8MaxCtas, &s_last);
+    }
     __syncthreads();  // the merge is done with the shared memory
   }
-}
-
-// Units cut into pieces, and heads without tokens: one CTA per (row tile, head).  Every
-// CTA lays out the same split again (the lengths have not changed), turns the pieces'
-// maxima and sums, all fetched at once, into one weight per (row, piece), and adds the
-// pieces' outputs in their order with eight fetches in flight.
-constexpr int kMergeThreads = 256;
-template <int D, typename T>
-__global__ void __launch_bounds__(kMergeThreads) q8_merge_rows_kernel(const Q8AttendArgs a, int tile_rows, int tile,
-                                                                      int grid, int min_tiles) {
-  __shared__ Q8Sched sch;
-  __shared__ float s_w[kRows][kQ8MaxCtas], s_l[kRows][kQ8MaxCtas];
-  pdl_wait();
-  pdl_trigger();
-  const int nrt = (a.Nq + tile_rows - 1) / tile_rows;
-  q8_build_sched(&sch, a.c.len, a.c.cap, a.c.H, nrt, tile, 1, 1, grid, min_tiles);
-  Q8Split S{&sch, a.c.H, nrt, 1, 1};
-  const int r = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
-  const int rows = min(tile_rows, a.Nq - r * tile_rows);
-  const size_t row0 = static_cast<size_t>(h) * a.Nq + r * tile_rows;
-  constexpr size_t kSlot = static_cast<size_t>(kRows) * D + 2 * kRows;
-  T* O = static_cast<T*>(a.O);
-  auto put = [&](int row, int c, float4 v) {
-    T* p = O + (row0 + row) * D + c;
-    if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-    else *reinterpret_cast<float4*>(p) = v;
-  };
-  if (sch.T[h] == 0) {
-    for (int i = tid; i < rows * (D / 4); i += kMergeThreads) put(i / (D / 4), (i % (D / 4)) * 4, make_float4(0.f, 0.f, 0.f, 0.f));
-    if (a.lse)
-      for (int i = tid; i < rows; i += kMergeThreads) a.lse[row0 + i] = -INFINITY;
-    return;
-  }
-  Q8Piece pc;
-  q8_unit_pieces(S, h, r, pc);
-  const int np = pc.npieces;
-  if (np == 1) return;
-  const float* first = a.part + static_cast<size_t>(pc.cfirst * 2 + pc.wfirst) * kSlot;
-  const float* rest = a.part + static_cast<size_t>(pc.cfirst) * 2 * kSlot;  // piece k > 0: slot 0 of CTA cfirst + k
-  auto slot = [&](int k) { return k == 0 ? first : rest + static_cast<size_t>(k) * 2 * kSlot; };
-  for (int i = tid; i < rows * np; i += kMergeThreads) {
-    const int row = i / np, k = i - row * np;
-    s_w[row][k] = __ldg(slot(k) + kRows * D + row);
-    s_l[row][k] = __ldg(slot(k) + kRows * D + kRows + row);
-  }
-  __syncthreads();
-  const int warp = tid >> 5, lane = tid & 31;
-  for (int row = warp; row < rows; row += kMergeThreads / 32) {
-    float M = -INFINITY;
-    for (int k = lane; k < np; k += 32) M = fmaxf(M, s_w[row][k]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float L = 0.f;
-    for (int k = lane; k < np; k += 32) {
-      const float f = M == -INFINITY ? 1.f : exp2f(s_w[row][k] - M);
-      s_w[row][k] = f;
-      L = fmaf(f, s_l[row][k], L);
-    }
-    L = warp_sum(L);
-    if (lane == 0) {
-      s_l[row][0] = 1.f / L;
-      if (a.lse) a.lse[row0 + row] = (M + log2f(L)) * kLn2;
-    }
-  }
-  __syncthreads();
-  for (int i = tid; i < rows * (D / 4); i += kMergeThreads) {
-    const int row = i / (D / 4), c = (i % (D / 4)) * 4;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < np; k0 += 8) {
-      float4 x[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u)
-        if (k0 + u < np) x[u] = __ldg(reinterpret_cast<const float4*>(slot(k0 + u) + row * D + c));
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        if (k0 + u >= np) continue;
-        const float f = s_w[row][k0 + u];
-        acc.x = fmaf(f, x[u].x, acc.x);
-        acc.y = fmaf(f, x[u].y, acc.y);
-        acc.z = fmaf(f, x[u].z, acc.z);
-        acc.w = fmaf(f, x[u].w, acc.w);
-      }
-    }
-    const float inv = s_l[row][0];
-    put(row, c, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-  }
+  empty_rows<D, __nv_bfloat16>(a, sch, kRows, nrt);
 }
 
 // ------------------------------------------------------------------ f32 rows
@@ -594,7 +573,8 @@ __device__ __forceinline__ float octet_sum(float v) {
 
 template <int D>
 __global__ void __launch_bounds__(kF32Threads) q8_attend_f32_kernel(const Q8AttendArgs a) {
-  extern __shared__ uint8_t smem[];
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int s_last;
   __shared__ Q8Sched sch;
   __shared__ float sm[kF32Groups][kF32Rows], sl[kF32Groups][kF32Rows];
   float* so = reinterpret_cast<float*>(smem);  // [group][row][D]
@@ -687,7 +667,13 @@ __global__ void __launch_bounds__(kF32Threads) q8_attend_f32_kernel(const Q8Atte
         }
       }
     }
+    if (pc.npieces > 1) {
+      __syncthreads();  // the groups' outputs have been read
+      finish_unit<D, float, kF32Rows>(a, pc, row0, rows, 0.f, so, so + kF32Rows * kQ8MaxCtas, &s_last);
+    }
+    __syncthreads();  // the merge is done with the shared memory
   }
+  empty_rows<D, float>(a, sch, kF32Rows, nrt);
 }
 
 // ------------------------------------------------------------------ weights
@@ -716,7 +702,8 @@ __global__ void __launch_bounds__(kThreads) q8_mass_rows_kernel(const Q8MassArgs
       const size_t row0 = static_cast<size_t>(h) * a.Nq + r0;
       const int rows = min(kRows, a.Nq - r0);
       QFrag<D, FEW> q;
-      q.load(static_cast<const __nv_bfloat16*>(a.Q) + row0 * D, rows, a.scale, g, t);
+      q.fetch(static_cast<const __nv_bfloat16*>(a.Q) + row0 * D, rows, g, t);
+      q.widen(a.scale);
       float z[kI];
 #pragma unroll
       for (int i = 0; i < kI; ++i) {
@@ -807,33 +794,22 @@ int split_grid(int n_sm) { return n_sm < kQ8MaxCtas ? n_sm : kQ8MaxCtas; }
 template <int D, bool FEW>
 cudaError_t attend_rows(const Q8AttendArgs& a, int n_sm, cudaStream_t st) {
   const int grid = split_grid(n_sm);
-  constexpr size_t smem = kWarps * kRing * 64 * D > sizeof(RowsShared<D>) ? kWarps * kRing * 64 * D : sizeof(RowsShared<D>);
-  cudaError_t e = cudaFuncSetAttribute(q8_attend_rows_kernel<D, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  constexpr size_t ring = kWarps * kRing * 64 * D, shared = sizeof(RowsShared<D>);
+  constexpr size_t smem = ring > shared ? ring : shared;
+  static_assert(smem >= 2 * kRows * kQ8MaxCtas * sizeof(float), "the merge's weights fit");
+  const cudaError_t e = cudaFuncSetAttribute(q8_attend_rows_kernel<D, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  {
-    LaunchTrace trace("q8_attend_rows_kernel", st);
-    e = launch_pdl(q8_attend_rows_kernel<D, FEW>, dim3(grid), dim3(kThreads), smem, st, a);
-  }
-  if (e != cudaSuccess) return e;
-  LaunchTrace trace("q8_merge_rows_kernel", st);
-  return launch_pdl(q8_merge_rows_kernel<D, __nv_bfloat16>, dim3((a.Nq + kRows - 1) / kRows, a.c.H), dim3(kMergeThreads), 0, st, a,
-                    static_cast<int>(kRows), static_cast<int>(kTile), grid, static_cast<int>(kMinTiles));
+  LaunchTrace trace("q8_attend_rows_kernel", st);
+  return launch_pdl(q8_attend_rows_kernel<D, FEW>, dim3(grid), dim3(kThreads), smem, st, a);
 }
 
 template <int D>
 cudaError_t attend_f32(const Q8AttendArgs& a, int n_sm, cudaStream_t st) {
-  const int grid = split_grid(n_sm);
-  const size_t smem = static_cast<size_t>(kF32Groups) * kF32Rows * D * sizeof(float);
-  cudaError_t e;
-  {
-    LaunchTrace trace("q8_attend_f32_kernel", st);
-    e = launch_pdl(q8_attend_f32_kernel<D>, dim3(grid), dim3(kF32Threads), smem, st, a);
-  }
-  if (e != cudaSuccess) return e;
-  LaunchTrace trace("q8_merge_rows_kernel", st);
-  return launch_pdl(q8_merge_rows_kernel<D, float>, dim3((a.Nq + kF32Rows - 1) / kF32Rows, a.c.H), dim3(kMergeThreads), 0, st, a,
-                    static_cast<int>(kF32Rows), static_cast<int>(kTile), grid, static_cast<int>(kMinTiles));
+  constexpr size_t smem = static_cast<size_t>(kF32Groups) * kF32Rows * D * sizeof(float);
+  static_assert(smem >= 2 * kF32Rows * kQ8MaxCtas * sizeof(float), "the merge's weights fit");
+  LaunchTrace trace("q8_attend_f32_kernel", st);
+  return launch_pdl(q8_attend_f32_kernel<D>, dim3(split_grid(n_sm)), dim3(kF32Threads), smem, st, a);
 }
 
 // CTAs per head so that the grid is about `waves` waves, no more than the tokens need
