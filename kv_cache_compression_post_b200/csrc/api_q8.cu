@@ -34,11 +34,11 @@ Q8View view(const kvb_q8_cache* c) {
 
 bool dtype_ok(kvb_dtype t) { return t == KVB_BF16 || t == KVB_F32; }
 
-// One scratch serves every call on a cache: the row-tile kernels' arrival counters, which
-// nothing else may write, then their partials, the positions an eviction keeps, or what a
+// One scratch serves every call on a cache: the row-tile kernels' piece flags, which
+// nothing else writes, then their partials, the positions an eviction keeps, or what a
 // chunk of queries needs, each from there.
 struct Scratch {
-  unsigned long long* cnt = nullptr;
+  unsigned long long* flag = nullptr;
   float* part = nullptr;
   int* kept = nullptr;
   Q8ChunkScratch chunk{};
@@ -50,7 +50,7 @@ bool chunk_kernel(int32_t rows, kvb_dtype dtype) { return dtype == KVB_BF16 && r
 Scratch scratch(const kvb_q8_cache* c, int32_t max_queries, kvb_dtype dtype, void* ws) {
   Scratch s;
   Carver a(ws);
-  s.cnt = a.take<unsigned long long>(kQ8RowCounters);
+  s.flag = a.take<unsigned long long>(kQ8RowFlags);
   Carver e = a, q = a;
   s.part = a.take<float>(q8_part_floats(c->head_dim));
   s.kept = e.take<int>(static_cast<size_t>(c->heads) * c->capacity);
@@ -66,6 +66,21 @@ Scratch scratch(const kvb_q8_cache* c, int32_t max_queries, kvb_dtype dtype, voi
     if (q.bytes() > s.bytes) s.bytes = q.bytes();
   }
   return s;
+}
+
+// A tag that no other call of this process has, and that memory which was never written
+// by one holds with probability 2^-64 (the calls' count through a bijective mixing of
+// shifts and odd products).
+unsigned long long next_tag() {
+  static std::atomic<unsigned long long> calls{0};
+  unsigned long long z = 0;
+  while (z == 0) {
+    z = (calls.fetch_add(1, std::memory_order_relaxed) + 1) * 0x9E3779B97F4A7C15ull;
+    z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
+    z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
+    z ^= z >> 31;
+  }
+  return z;
 }
 
 bool workspace_ok(const void* ws, size_t have, size_t want) { return ws && aligned(ws, 256) && have >= want; }
@@ -133,10 +148,8 @@ kvb_status kvb_q8_attend(const kvb_q8_cache* c, const void* Q, int32_t Nq, kvb_d
   a.O = O;
   a.lse = lse;
   a.part = s.part;
-  a.cnt = s.cnt;
-  static std::atomic<unsigned int> calls{0};
-  do a.epoch = calls.fetch_add(1, std::memory_order_relaxed) + 1;
-  while (a.epoch == 0);
+  a.flag = s.flag;
+  a.tag = next_tag();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == KVB_F32) return cuda_status(launch_q8_attend_f32(a, dev.n_sm, st));
   if (chunk_kernel(Nq, dtype)) return cuda_status(launch_q8_attend_chunk(a, s.chunk, dev.n_sm, st));

@@ -70,12 +70,18 @@ constexpr float kLn2 = 0.6931471805599453f;
 // [ceil(c total / G), ceil((c+1) total / G)).  Heads of very different length, one
 // row or many, thus load every SM alike.  A unit cut between CTAs leaves one partial
 // per piece: in a CTA's slot 0 for its first piece, slot 1 for its last one.
+// Where there are at most half as many units as CTAs (chunk > 0) no CTA takes parts of
+// two units: each unit is cut into ceil(T / chunk) equal pieces, chunk such that the CTAs
+// suffice, and a CTA has one piece.  A CTA's second piece begins when its
+// first is done, with every latency of a beginning once more: 4 of 25 us for 12 heads of
+// 15600 tokens.
 struct Q8Sched {
-  long long C[kQ8MaxHeads + 1];  // cost before each head
+  long long C[kQ8MaxHeads + 1];  // cost before each head (chunk > 0: CTAs)
   int T[kQ8MaxHeads];
   long long total;
   int G;
   bool small;  // total * G < 2^32: 32-bit quotients do (a 64-bit one takes ~400 clk)
+  int chunk;
 };
 
 struct Q8Split {
@@ -98,15 +104,25 @@ struct Q8Split {
 // Filled by the whole CTA (blockDim.x a multiple of 32); `min_cost`: a CTA's share is
 // at least this much.  Ends with a __syncthreads().
 __device__ __forceinline__ void q8_build_sched(Q8Sched* s, const int* len, int cap, int H, int nrt, int tile, int w,
-                                               int wlast, int grid, int min_cost) {
+                                               int wlast, int grid, int min_cost, bool may_chunk = false) {
   for (int h = threadIdx.x; h < H; h += blockDim.x) s->T[h] = (q8_len(len, h, cap) + tile - 1) / tile;
   __syncthreads();
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
-    const long long per = static_cast<long long>(nrt - 1) * w + wlast;
+    long long per = static_cast<long long>(nrt - 1) * w + wlast;
+    int chunk = 0;
+    if (may_chunk && static_cast<long long>(H) * nrt * 2 <= grid) {
+      int sum = 0;  // key tiles of all units: below 2^25 tokens x heads
+      for (int h = lane; h < H; h += 32) sum += s->T[h] * nrt;
+      sum = warp_sum_int(sum);
+      // sum / chunk pieces, and at most one more per unit: no more than the CTAs
+      const int spare = grid - H * nrt;
+      chunk = max(min_cost, (sum + spare - 1) / spare);
+    }
     long long carry = 0;
     for (int b = 0; b < H; b += 32) {
-      const long long n = b + lane < H ? per * s->T[b + lane] : 0;
+      long long n = b + lane < H ? per * s->T[b + lane] : 0;
+      if (chunk > 0 && b + lane < H) n = static_cast<long long>((s->T[b + lane] + chunk - 1) / chunk) * nrt;
       long long x = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -121,6 +137,8 @@ __device__ __forceinline__ void q8_build_sched(Q8Sched* s, const int* len, int c
       s->total = carry;
       const long long g = carry / min_cost;
       s->G = static_cast<int>(g < 1 ? 1 : (g < grid ? g : grid));
+      s->chunk = chunk;
+      if (chunk > 0) s->G = static_cast<int>(carry < 1 ? 1 : carry);
       s->small = (carry + 1) * (s->G + 1) < (1ll << 32);
     }
   }
@@ -164,6 +182,17 @@ struct Q8Walk {
     first = true;
     h = S.H;
     if (S.s->total <= 0 || cta >= S.s->G) return;
+    if (S.s->chunk > 0) {
+      int a = 0, b = S.H;  // the last head with C[h] <= cta
+      while (b - a > 1) {
+        const int m = (a + b) / 2;
+        if (S.s->C[m] <= cta) a = m;
+        else b = m;
+      }
+      h = a;
+      hi = cta;
+      return;
+    }
     const long long x = S.lo(cta);
     hi = S.lo(cta + 1);
     int a = 0, b = S.H;  // the last head with C[h] <= x
@@ -189,6 +218,19 @@ struct Q8Walk {
   // whole: with the unit's pieces (a caller in a hurry finds them later, q8_unit_pieces)
   __device__ bool next(const Q8Split& S, Q8Piece& pc, bool whole = true) {
     if (h >= S.H) return false;
+    if (S.s->chunk > 0) {  // one piece
+      const uint32_t T = S.s->T[h], np = (T + S.s->chunk - 1) / S.s->chunk;
+      const uint32_t i = static_cast<uint32_t>(hi - S.s->C[h]), unit = i / np, k = i - unit * np;
+      pc.h = h;
+      pc.r = unit;
+      pc.j0 = static_cast<int>(k * T / np);  // T <= 2^18, np <= 160
+      pc.j1 = static_cast<int>((k + 1) * T / np);
+      pc.npieces = np;
+      pc.which = pc.wfirst = 0;
+      pc.cfirst = static_cast<int>(hi - k);
+      h = S.H;
+      return true;
+    }
     const long long cu = S.start(h, r);
     const int w = S.wt(r);
     if (cu + static_cast<long long>(w) * j >= hi) return false;
@@ -216,8 +258,8 @@ struct Q8AttendArgs {
   void* O;
   float* lse;
   float* part;  // partials: q8_part_floats(d) floats
-  unsigned long long* cnt;  // the row-tile kernels' arrival counters: kQ8RowCounters
-  unsigned int epoch;       // of this launch, nonzero
+  unsigned long long* flag;  // the row-tile kernels' piece flags: kQ8RowFlags
+  unsigned long long tag;    // of this call, nonzero
 };
 
 struct Q8MassArgs {
@@ -236,7 +278,7 @@ cudaError_t launch_q8_attend_f32(const Q8AttendArgs& a, int n_sm, cudaStream_t s
 cudaError_t launch_q8_mass_rows(const Q8MassArgs& a, int n_sm, cudaStream_t st);
 cudaError_t launch_q8_mass_f32(const Q8MassArgs& a, int n_sm, cudaStream_t st);
 
-constexpr int kQ8RowCounters = kQ8MaxCtas * 2;
+constexpr int kQ8RowFlags = kQ8MaxCtas * 2;
 // floats of partials the row-tile kernels need: two slots per CTA of 16 rows and
 // their maxima and sums
 inline size_t q8_part_floats(int d) { return static_cast<size_t>(kQ8MaxCtas) * 2 * (16 * d + 32); }

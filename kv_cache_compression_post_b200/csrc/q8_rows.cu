@@ -229,19 +229,24 @@ struct RowsShared {
   float m[kWarps][kRows], l[kWarps][kRows];
 };
 
-// Arrival at a cut unit's counter: true for the last of its pieces, which resets it.  The
-// count is tagged with the launch's epoch, so the counters need no initialisation; a
-// replayed launch finds them reset by its earlier run.
-__device__ __forceinline__ bool arrive_last(unsigned long long* cp, unsigned int epoch, int npieces) {
-  unsigned long long cur = *reinterpret_cast<volatile unsigned long long*>(cp);
-  for (;;) {  // every failed exchange is another piece's success: at most npieces rounds
-    const unsigned int have = static_cast<unsigned int>(cur >> 32) == epoch ? static_cast<unsigned int>(cur) : 0u;
-    const bool fin = have + 1 >= static_cast<unsigned int>(npieces);
-    const unsigned long long want = fin ? 0ull : (static_cast<unsigned long long>(epoch) << 32) | (have + 1);
-    const unsigned long long was = atomicCAS(cp, cur, want);
-    if (was == cur) return fin;
-    cur = was;
-  }
+// Whether every piece of a cut unit is there, this CTA's included, which it says first.
+// Each piece has a flag of its own, set to the call's tag: no counter that pieces ending
+// together queue up for (compare-and-swap on one took 8 us for 12 of them), nothing to
+// initialise.  Every lane's fence lies between the setting and its looks at the others,
+// and fences have one order: the piece whose fences come last sees all flags.  More than
+// one may; they write the same values.  Whoever sees them all clears them, so that a
+// replayed call finds none of its earlier run.  Called by one warp.
+__device__ __forceinline__ bool all_there(unsigned long long* flag, unsigned long long tag, const Q8Piece& pc, int lane) {
+  volatile unsigned long long* f = flag;
+  if (lane == 0) f[blockIdx.x * 2 + pc.which] = tag;
+  __syncwarp();
+  __threadfence();
+  bool all = true;
+  for (int k = lane; k < pc.npieces; k += 32) all &= f[(pc.cfirst + k) * 2 + (k == 0 ? pc.wfirst : 0)] == tag;
+  all = __all_sync(0xffffffffu, all);
+  if (all)
+    for (int k = lane; k < pc.npieces; k += 32) f[(pc.cfirst + k) * 2 + (k == 0 ? pc.wfirst : 0)] = 0ull;
+  return all;
 }
 
 template <typename T, int D>
@@ -251,7 +256,7 @@ __device__ __forceinline__ void put_row4(void* O, size_t row, int c, float4 v) {
   else *reinterpret_cast<float4*>(p) = v;
 }
 
-// The last piece of a unit to arrive merges them all, in their order: the pieces' maxima
+// A piece that finds all pieces of its unit there merges them, in their order: their maxima
 // and sums, fetched at once, become one weight per (row, piece); then the outputs, with
 // eight fetches in flight.  (A second kernel for it cost 6 us.)  Called by the whole CTA
 // after it has stored its own piece; s_w, s_l: shared memory, ROWS x kQ8MaxCtas each.
@@ -261,7 +266,10 @@ __device__ void finish_unit(const Q8AttendArgs& a, const Q8Piece& pc, size_t row
   const int tid = threadIdx.x, nthreads = blockDim.x, np = pc.npieces;
   __threadfence();
   __syncthreads();
-  if (tid == 0) *s_last = arrive_last(a.cnt + pc.cfirst * 2 + pc.wfirst, a.epoch, np) ? 1 : 0;
+  if (tid < 32) {
+    const bool all = all_there(a.flag, a.tag, pc, tid);
+    if (tid == 0) *s_last = all;
+  }
   __syncthreads();
   if (!*s_last) return;
   __threadfence();
@@ -348,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_rows_kernel(const Q8Att
   pdl_wait();
   pdl_trigger();
   const int nrt = (a.Nq + kRows - 1) / kRows;
-  q8_build_sched(&sch, a.c.len, a.c.cap, a.c.H, nrt, kTile, 1, 1, gridDim.x, kMinTiles);
+  q8_build_sched(&sch, a.c.len, a.c.cap, a.c.H, nrt, kTile, 1, 1, gridDim.x, kMinTiles, true);
   Q8Split S{&sch, a.c.H, nrt, 1, 1};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int blocks = a.c.cap >> a.c.shift;
@@ -387,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_rows_kernel(const Q8Att
       }
     };
     scales(first);
-    q8_unit_pieces(S, pc.h, pc.r, pc);
+    if (sch.chunk == 0) q8_unit_pieces(S, pc.h, pc.r, pc);
     q.widen(a.scale);
     float o[D / 8][4];  // FEW: rows g + 8 stay 0
 #pragma unroll
@@ -581,7 +589,7 @@ __global__ void __launch_bounds__(kF32Threads) q8_attend_f32_kernel(const Q8Atte
   pdl_wait();
   pdl_trigger();
   const int nrt = (a.Nq + kF32Rows - 1) / kF32Rows;
-  q8_build_sched(&sch, a.c.len, a.c.cap, a.c.H, nrt, kTile, 1, 1, gridDim.x, kMinTiles);
+  q8_build_sched(&sch, a.c.len, a.c.cap, a.c.H, nrt, kTile, 1, 1, gridDim.x, kMinTiles, true);
   Q8Split S{&sch, a.c.H, nrt, 1, 1};
   const int grp = threadIdx.x >> 3, sub = threadIdx.x & 7;
   const int blocks = a.c.cap >> a.c.shift;
