@@ -33,7 +33,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 
 struct SelShared {
   uint32_t key[kSelKeys];
-  int hist[kCopies][256];
+  int hist[kCopies][257];  // a bin's copies in different banks
   int sum[2][256];     // this CTA's digit counts, by parity of the pass
   int total[256];      // the head's
   int above[kSelWarps], equal[kSelWarps];
@@ -79,7 +79,7 @@ __global__ void __cluster_dims__(kSelCtas, 1, 1) __launch_bounds__(kSelThreads) 
     const int p0 = max(c0, lo), p1 = min(c1, hi);
     for (int pass = 0; pass < 4; ++pass) {
       const int shift = 24 - 8 * pass;
-      for (int i = tid; i < kCopies * 256; i += kSelThreads) (&s.hist[0][0])[i] = 0;
+      for (int i = tid; i < kCopies * 257; i += kSelThreads) (&s.hist[0][0])[i] = 0;
       __syncthreads();
       const uint32_t prefix = s.prefix;
       const int want = s.need;
