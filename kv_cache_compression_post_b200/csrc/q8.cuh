@@ -249,6 +249,14 @@ struct Q8Walk {
   }
 };
 
+// The first r with (h * n + r) % G == blockIdx.x: this CTA's first turn at n things of
+// head h that all CTAs share out.
+__device__ __forceinline__ int q8_first_turn(int h, int n, int G) {
+  const int at = static_cast<int>(static_cast<long long>(h) * n % G);
+  const int r = static_cast<int>(blockIdx.x) - at;
+  return r < 0 ? r + G : r;
+}
+
 // ------------------------------------------------------------------ launchers
 struct Q8AttendArgs {
   Q8View c;
@@ -300,9 +308,18 @@ cudaError_t launch_q8_mass_chunk(const Q8MassArgs& a, const Q8ChunkScratch& s, i
 constexpr int kQ8MassCounters = kQ8MaxCtas * 2 * 8;  // arrival counters of the weights' cut blocks
 cudaError_t launch_q8_attend_chunk(const Q8AttendArgs& a, const Q8ChunkScratch& s, int n_sm, cudaStream_t st);
 
-// Rows per head from which a bf16 call takes the tensor-core chunk kernel instead of
-// the 16-row tiles.
-constexpr int kQ8ChunkRows = 17;
+// Rows per head from which a bf16 call takes the tcgen05 kernel (128 or 256 rows at once,
+// however few there are) instead of 16-row tiles, each of which reads the cache again.
+// us measured, 16-row tiles / tcgen05, head_dim 128:
+//   attention   heads x tokens   32 rows     48 rows     64 rows     128 rows
+//               12 x 15600       37 / 62     47 / 62     57 / 62     104 / 64
+//               8 x 131072       129 / 160   183 / 160   265 / 162   509 / 160
+//               1 x 8192         18 / 37     18 / 37     19 / 37     19 / 38
+//               64 x 1024        32 / 46     40 / 46     45 / 46     71 / 49
+//   weights     12 x 15600       21 / 27     27 / 27     33 / 27     57 / 27
+//               8 x 131072       84 / 111    110 / 112   137 / 112   242 / 112
+//               64 x 1024        9 / 16      11 / 16     14 / 16     22 / 16
+constexpr int kQ8ChunkRows = 49;
 
 struct Q8EvictArgs {
   Q8View src;

@@ -334,8 +334,7 @@ template <int D, typename T>
 __device__ void empty_rows(const Q8AttendArgs& a, const Q8Sched& sch, int tile_rows, int nrt) {
   for (int h = 0; h < a.c.H; ++h) {
     if (sch.T[h] != 0) continue;
-    for (int r = 0; r < nrt; ++r) {
-      if ((h * nrt + r) % sch.G != static_cast<int>(blockIdx.x)) continue;
+    for (int r = q8_first_turn(h, nrt, sch.G); r < nrt; r += sch.G) {
       const int rows = min(tile_rows, a.Nq - r * tile_rows);
       const size_t row0 = static_cast<size_t>(h) * a.Nq + r * tile_rows;
       for (int i = threadIdx.x; i < rows * (D / 4); i += blockDim.x)
@@ -687,10 +686,28 @@ __global__ void __launch_bounds__(kF32Threads) q8_attend_f32_kernel(const Q8Atte
 // ------------------------------------------------------------------ weights
 // mass[k] = decay prev[k] + sum over rows of 2^(x - lse log2 e): a token's weight is
 // whole within its warp, so there is nothing to split or merge, and the rows are added
-// in one fixed order.  Reads K once per 16 rows (the first time from memory).
+// in one fixed order.  Up to sixteen rows (ONE) stay in registers for all of a warp's
+// tokens; of more, each step fetches them again, 16 at a time.  FEW: at most eight.
 template <int D, bool FEW>
-__global__ void __launch_bounds__(kThreads) q8_mass_rows_kernel(const Q8MassArgs a) {
-  constexpr int kI = FEW ? 1 : 2;
+struct WeightRows {
+  static constexpr int kI = FEW ? 1 : 2;
+  QFrag<D, FEW> q;
+  float z[kI];  // -lse log2 e; -inf: no such row, or one that saw nothing, which weighs nothing
+  __device__ __forceinline__ void load(const Q8MassArgs& a, int h, int r0, int g, int t) {
+    const size_t row0 = static_cast<size_t>(h) * a.Nq + r0;
+    const int rows = min(kRows, a.Nq - r0);
+    q.fetch(static_cast<const __nv_bfloat16*>(a.Q) + row0 * D, rows, g, t);
+#pragma unroll
+    for (int i = 0; i < kI; ++i) {
+      const float v = g + 8 * i < rows ? a.lse[row0 + g + 8 * i] : -INFINITY;
+      z[i] = v == -INFINITY ? -INFINITY : -v * kLog2e;
+    }
+    q.widen(a.scale);
+  }
+};
+
+template <int D, bool FEW, bool ONE>
+__global__ void __launch_bounds__(kThreads, FEW ? 2 : 1) q8_mass_rows_kernel(const Q8MassArgs a) {
   pdl_wait();
   pdl_trigger();
   const int h = blockIdx.y;
@@ -698,46 +715,46 @@ __global__ void __launch_bounds__(kThreads) q8_mass_rows_kernel(const Q8MassArgs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const uint8_t* K = a.c.K + static_cast<size_t>(h) * a.c.cap * D;
   const float* ks = a.c.ks + static_cast<size_t>(h) * (a.c.cap >> a.c.shift);
-  for (int kb = (blockIdx.x * kWarps + warp) * kSub; kb < n; kb += gridDim.x * kWarps * kSub) {
-    KWords<D> kw;
-    kw.load_global(K, kb, n - 1, g, t);
-    float kf[2], w[4][2];
+  const size_t m0 = static_cast<size_t>(h) * a.c.cap;
+  const int hop = gridDim.x * kWarps * kSub;
+  int kb = (blockIdx.x * kWarps + warp) * kSub;
+  if (kb >= n) return;
+  KWords<D> next;
+  next.load_global(K, kb, n - 1, g, t);
+  WeightRows<D, FEW> rows;
+  if constexpr (ONE) rows.load(a, h, 0, g, t);
+  // lane (g, t) stores tokens 8 j + 2 t + i where g = 2 j + i, and fetches what it adds to
+  const int mine = 8 * (g >> 1) + 2 * t + (g & 1);
+  for (; kb < n; kb += hop) {
+    const KWords<D> kw = next;
+    float kf[2], w[4][2], before = 0.f;
 #pragma unroll
     for (int u = 0; u < 2; ++u) kf[u] = __ldg(ks + (min(kb + 16 * u, n - 1) >> a.c.shift));
+    if (a.prev && kb + mine < n) before = a.prev[m0 + kb + mine];
+    if (kb + hop < n) next.load_global(K, kb + hop, n - 1, g, t);
 #pragma unroll
     for (int j = 0; j < 4; ++j) w[j][0] = w[j][1] = 0.f;
-    for (int r0 = 0; r0 < a.Nq; r0 += kRows) {
-      const size_t row0 = static_cast<size_t>(h) * a.Nq + r0;
-      const int rows = min(kRows, a.Nq - r0);
-      QFrag<D, FEW> q;
-      q.fetch(static_cast<const __nv_bfloat16*>(a.Q) + row0 * D, rows, g, t);
-      q.widen(a.scale);
-      float z[kI];
-#pragma unroll
-      for (int i = 0; i < kI; ++i) {
-        const float v = g + 8 * i < rows ? a.lse[row0 + g + 8 * i] : -INFINITY;
-        z[i] = v == -INFINITY ? -INFINITY : -v * kLog2e;  // a row of lse -inf weighs nothing
-      }
+    for (int r0 = 0; r0 < (ONE ? 1 : a.Nq); r0 += kRows) {
+      if constexpr (!ONE) rows.load(a, h, r0, g, t);
       float s[4][4];
-      kw.template dots<FEW>(q, s);
+      kw.template dots<FEW>(rows.q, s);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int k = 0; k < 2 * kI; ++k) w[j][k & 1] += ex2_approx(fmaf(s[j][k], q.coef[k >> 1] * kf[j >> 1], z[k >> 1]));
+        for (int k = 0; k < 2 * WeightRows<D, FEW>::kI; ++k)
+          w[j][k & 1] += ex2_approx(fmaf(s[j][k], rows.q.coef[k >> 1] * kf[j >> 1], rows.z[k >> 1]));
     }
+    float v = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float v = w[j][i];
+        float x = w[j][i];
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        const int key = kb + 8 * j + 2 * t + i;
-        if (g == 2 * j + i && key < n) {
-          const size_t at = static_cast<size_t>(h) * a.c.cap + key;
-          a.mass[at] = a.prev ? fmaf(a.decay, a.prev[at], v) : v;
-        }
+        for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (g == 2 * j + i) v = x;
       }
+    if (kb + mine < n) a.mass[m0 + kb + mine] = a.prev ? fmaf(a.decay, before, v) : v;
   }
 }
 
@@ -839,11 +856,15 @@ cudaError_t launch_q8_attend_f32(const Q8AttendArgs& a, int n_sm, cudaStream_t s
 cudaError_t launch_q8_mass_rows(const Q8MassArgs& a, int n_sm, cudaStream_t st) {
   const dim3 grid(mass_blocks(a.c.cap, kWarps * kSub, a.c.H, n_sm, 2), a.c.H);
   LaunchTrace trace("q8_mass_rows_kernel", st);
+  const bool wide = a.c.d == 128;
   if (a.Nq <= 8)
-    return a.c.d == 128 ? launch_pdl(q8_mass_rows_kernel<128, true>, grid, dim3(kThreads), 0, st, a)
-                        : launch_pdl(q8_mass_rows_kernel<64, true>, grid, dim3(kThreads), 0, st, a);
-  return a.c.d == 128 ? launch_pdl(q8_mass_rows_kernel<128, false>, grid, dim3(kThreads), 0, st, a)
-                      : launch_pdl(q8_mass_rows_kernel<64, false>, grid, dim3(kThreads), 0, st, a);
+    return wide ? launch_pdl(q8_mass_rows_kernel<128, true, true>, grid, dim3(kThreads), 0, st, a)
+                : launch_pdl(q8_mass_rows_kernel<64, true, true>, grid, dim3(kThreads), 0, st, a);
+  if (a.Nq <= kRows)
+    return wide ? launch_pdl(q8_mass_rows_kernel<128, false, true>, grid, dim3(kThreads), 0, st, a)
+                : launch_pdl(q8_mass_rows_kernel<64, false, true>, grid, dim3(kThreads), 0, st, a);
+  return wide ? launch_pdl(q8_mass_rows_kernel<128, false, false>, grid, dim3(kThreads), 0, st, a)
+              : launch_pdl(q8_mass_rows_kernel<64, false, false>, grid, dim3(kThreads), 0, st, a);
 }
 cudaError_t launch_q8_mass_f32(const Q8MassArgs& a, int n_sm, cudaStream_t st) {
   const dim3 grid(mass_blocks(a.c.cap, kThreads / 8 * kF32Keys, a.c.H, n_sm, 4), a.c.H);

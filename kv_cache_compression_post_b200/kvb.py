@@ -342,11 +342,23 @@ def _tensor_dtype(x, where: str) -> int:
     raise KvbError(1, where)
 
 
-def _rows(x, shape, dtype, where: str):
-    """The head and token strides of a [heads][n][d] device tensor of a call, in any order
-    of its rows: its shape and type are checked, and that a row is contiguous.  The stride
-    of a dimension of one row says nothing and counts as 0."""
-    if x.shape != shape or x.dtype is not dtype or not x.is_cuda:
+def _device(device, where: str) -> int:
+    """The current device's ordinal, which has to be `device` where that is given: a kernel
+    runs on the current device, and its tensors have to lie there."""
+    import torch
+    if not torch.cuda.is_initialized():
+        raise KvbError(1, where)
+    now = torch._C._cuda_getDevice()
+    if device is not None and now != device:
+        raise KvbError(1, where)
+    return now
+
+
+def _rows(x, shape, dtype, device: int, where: str):
+    """The head and token strides of a [heads][n][d] tensor of a call, in any order of its
+    rows: its shape, type and device are checked, and that a row is contiguous.  The
+    stride of a dimension of one row says nothing and counts as 0."""
+    if x.shape != shape or x.dtype is not dtype or x.get_device() != device:
         raise KvbError(1, where)
     h, n, e = x.stride()
     if e != 1 and shape[2] != 1:
@@ -354,11 +366,11 @@ def _rows(x, shape, dtype, where: str):
     return (h if shape[0] > 1 else 0), (n if shape[1] > 1 else 0)
 
 
-def _whole(x, shape, dtype, where: str) -> int:
-    """The address of a contiguous device tensor of a call, checked (None passes, as 0)."""
+def _whole(x, shape, dtype, device: int, where: str) -> int:
+    """The address of a contiguous tensor of a call, checked (None passes, as 0)."""
     if x is None:
         return 0
-    if x.shape != shape or x.dtype is not dtype or not x.is_cuda or not x.is_contiguous():
+    if x.shape != shape or x.dtype is not dtype or x.get_device() != device or not x.is_contiguous():
         raise KvbError(1, where)
     return x.data_ptr()
 
@@ -369,12 +381,13 @@ def rope(X, pos, out, axis_pairs, base: float = 10000.0, pairing: int = KVB_ROPE
     token-major tensor, say), both of one type; pos int32 [tokens][3]."""
     import torch
     dtype = _tensor_dtype(X, "kvb_rope")
+    dev = _device(None, "kvb_rope")
     if X.dim() != 3 or len(axis_pairs) != 3:
         raise KvbError(1, "kvb_rope")
     shape = X.shape
-    xh, xt = _rows(X, shape, X.dtype, "kvb_rope")
-    oh, ot = _rows(out, shape, X.dtype, "kvb_rope")
-    st = lib.kvb_rope(X.data_ptr(), _whole(pos, (shape[1], 3), torch.int32, "kvb_rope"), shape[0], shape[1], shape[2],
+    xh, xt = _rows(X, shape, X.dtype, dev, "kvb_rope")
+    oh, ot = _rows(out, shape, X.dtype, dev, "kvb_rope")
+    st = lib.kvb_rope(X.data_ptr(), _whole(pos, (shape[1], 3), torch.int32, dev, "kvb_rope"), shape[0], shape[1], shape[2],
                       dtype, (_i32 * 3)(*axis_pairs), base, pairing, 1 if inverse else 0, xh, xt, out.data_ptr(), oh,
                       ot, _stream(stream))
     if st:
@@ -398,9 +411,11 @@ class Q8Cache:
         def own(x, shape, dt, make):
             if x is None:
                 return make(shape, dtype=dt, device="cuda")
-            _whole(x, shape, dt, "kvb_q8_cache")
+            _whole(x, shape, dt, self.device, "kvb_q8_cache")
             return x
 
+        torch.cuda.init()
+        self.device = _device(None, "kvb_q8_cache")
         if block not in (16, 32, 64, 128) or capacity % block:
             raise KvbError(1, "kvb_q8_cache")
         self.heads, self.head_dim, self.capacity, self.block = heads, head_dim, capacity, block
@@ -426,22 +441,24 @@ class Q8Cache:
     def append(self, K, V, start=None, stream=None) -> None:
         """kvb_q8_append: K, V [heads][n][d] in any row order; start int32 [heads] or None."""
         import torch
+        dev = _device(self.device, "kvb_q8_append")
         shape = (self.heads, K.shape[1] if K.dim() == 3 else -1, self.head_dim)
-        kh, kt = _rows(K, shape, self.torch_dtype, "kvb_q8_append")
-        vh, vt = _rows(V, shape, self.torch_dtype, "kvb_q8_append")
+        kh, kt = _rows(K, shape, self.torch_dtype, dev, "kvb_q8_append")
+        vh, vt = _rows(V, shape, self.torch_dtype, dev, "kvb_q8_append")
         st = lib.kvb_q8_append(self._ref, K.data_ptr(), kh, kt, V.data_ptr(), vh, vt, shape[1], self.dtype,
-                               _whole(start, (self.heads,), torch.int32, "kvb_q8_append"), _stream(stream))
+                               _whole(start, (self.heads,), torch.int32, dev, "kvb_q8_append"), _stream(stream))
         if st:
             raise KvbError(st, "kvb_q8_append")
 
     def attend(self, Q, O, lse=None, scale: float = 0.0, stream=None) -> None:
         """kvb_q8_attend: Q, O [heads][Nq][d], lse f32 [heads][Nq] or None."""
         import torch
+        dev = _device(self.device, "kvb_q8_attend")
         n = Q.shape[1] if Q.dim() == 3 else 0
         shape = (self.heads, n, self.head_dim)
-        st = lib.kvb_q8_attend(self._ref, _whole(Q, shape, self.torch_dtype, "kvb_q8_attend"), n, self.dtype, scale,
-                               _whole(O, shape, self.torch_dtype, "kvb_q8_attend"),
-                               _whole(lse, (self.heads, n), torch.float32, "kvb_q8_attend"), self.ws, self.nbytes,
+        st = lib.kvb_q8_attend(self._ref, _whole(Q, shape, self.torch_dtype, dev, "kvb_q8_attend"), n, self.dtype, scale,
+                               _whole(O, shape, self.torch_dtype, dev, "kvb_q8_attend"),
+                               _whole(lse, (self.heads, n), torch.float32, dev, "kvb_q8_attend"), self.ws, self.nbytes,
                                _stream(stream))
         if st:
             raise KvbError(st, "kvb_q8_attend")
@@ -450,19 +467,23 @@ class Q8Cache:
         """kvb_q8_mass: ``mass`` = decay * prev + the weights of these queries; prev None is
         the present ``mass``."""
         import torch
+        dev = _device(self.device, "kvb_q8_mass")
         n = Q.shape[1] if Q.dim() == 3 else 0
-        st = lib.kvb_q8_mass(self._ref, _whole(Q, (self.heads, n, self.head_dim), self.torch_dtype, "kvb_q8_mass"), n,
-                             self.dtype, scale, _whole(lse, (self.heads, n), torch.float32, "kvb_q8_mass"), decay,
-                             _whole(self.mass if prev is None else prev, (self.heads, self.capacity), torch.float32,
+        st = lib.kvb_q8_mass(self._ref, _whole(Q, (self.heads, n, self.head_dim), self.torch_dtype, dev, "kvb_q8_mass"), n,
+                             self.dtype, scale, _whole(lse, (self.heads, n), torch.float32, dev, "kvb_q8_mass"), decay,
+                             _whole(self.mass if prev is None else prev, (self.heads, self.capacity), torch.float32, dev,
                                     "kvb_q8_mass"), self.ws, self.nbytes, _stream(stream))
         if st:
             raise KvbError(st, "kvb_q8_mass")
 
     def evict(self, to: "Q8Cache", budget: int, sink: int = 0, recent: int = 0, kept=None, stream=None) -> None:
-        """kvb_q8_evict into another cache; kept int32 [heads][budget] or None."""
+        """kvb_q8_evict into another cache of the device; kept int32 [heads][budget] or None."""
         import torch
+        dev = _device(self.device, "kvb_q8_evict")
+        if to.device != dev:
+            raise KvbError(1, "kvb_q8_evict")
         st = lib.kvb_q8_evict(self._ref, to._ref, budget, sink, recent,
-                              _whole(kept, (self.heads, budget), torch.int32, "kvb_q8_evict"), self.ws, self.nbytes,
+                              _whole(kept, (self.heads, budget), torch.int32, dev, "kvb_q8_evict"), self.ws, self.nbytes,
                               _stream(stream))
         if st:
             raise KvbError(st, "kvb_q8_evict")

@@ -168,7 +168,7 @@ LENS = [0, 1, 15, 16, 17, 31, 63, 64, 65, 127, 128, 129, 500]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("rows", [1, 2, 8, 9, 16, 17, 33, 130])
+@pytest.mark.parametrize("rows", [1, 2, 8, 9, 16, 17, 33, 49, 130])
 @pytest.mark.parametrize("d,block", [(64, 16), (128, 64), (128, 128)])
 def test_attend_ragged_lengths(d, block, rows, dtype):
     import torch
@@ -527,3 +527,159 @@ def test_two_streams_and_two_caches_at_once():
         assert torch.equal(got[i][0], want[i][0]) and torch.equal(got[i][1], want[i][1])
         assert torch.equal(caches[i].mass.view(torch.int32), want[i][2].view(torch.int32))
         assert caches[i].status() == 0
+
+
+# ------------------------------------------------------------------ edges of the calls
+def test_captured_chunk_step_and_eviction():
+    """A captured step of a chunk (append, attend, accumulate, evict into a second cache) and
+    its replays, in a workspace that a second captured graph uses in turn."""
+    import torch
+    import kv_cache_compression_post_b200 as kvb
+    torch.manual_seed(21)
+    H, d, block, n, rows = 3, 128, 64, 300, 200
+    a = kvb.Q8Cache(H, d, 1024, block, max_queries=rows, with_mass=True)
+    b = kvb.Q8Cache(H, d, 512, block, max_queries=rows, with_mass=True)
+    b.ws, b._buf = a.ws, a._buf                       # one workspace, used one call after another
+    x = torch.randn(3, H, n, d, device="cuda").bfloat16()
+    Q = torch.randn(H, rows, d, device="cuda").bfloat16()
+    one = torch.randn(H, 2, d, device="cuda").bfloat16()
+    O, lse = torch.empty_like(Q), torch.empty(H, rows, device="cuda")
+    O2, lse2 = torch.empty_like(one), torch.empty(H, 2, device="cuda")
+
+    def chunk():
+        a.append(x[0], x[1])
+        a.attend(Q, O, lse)
+        a.accumulate(Q, lse)
+        a.evict(b, 256, sink=5, recent=20)
+
+    def token():
+        b.attend(one, O2, lse2)
+        b.accumulate(one, lse2, decay=0.5)
+
+    chunk(), token()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (O, lse, a.mass, b.K, b.V, b.mass, O2, lse2)]
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for g, f in zip(graphs, (chunk, token)):
+        with torch.cuda.graph(g):
+            f()
+    for _ in range(3):
+        a.len.zero_()
+        a.mass.zero_()
+        b.mass.zero_()
+        for g in graphs:
+            g.replay()
+        for got, w in zip((O, lse, a.mass, b.K, b.V, b.mass, O2, lse2), want):
+            if got is b.K or got is b.V:
+                got, w = got[:, :256], w[:, :256]
+            assert torch.equal(got, w)
+    assert a.status() == 0 and b.status() == 0
+    check_attend(a, Q, O, lse)
+    check_attend(b, one, O2, lse2)
+
+
+@pytest.mark.parametrize("rows", [1, 12, 40, 300])
+def test_workspace_needs_no_initialisation(rows):
+    """Whatever the workspace held, also between calls of another kind, changes nothing."""
+    import torch
+    torch.manual_seed(rows)
+    c = filled(2, 128, 8192, 64, "bf16", [8000, 5000], 3, max_queries=300)
+    Q = torch.randn(2, rows, 128, device="cuda").bfloat16()
+    O, lse = attend(c, Q)
+    prev = c.mass.clone()
+    c.accumulate(Q, lse, prev=prev)
+    mass = c.mass.clone()
+    for fill in (0, 255, None):
+        if fill is None:
+            c._buf.random_(0, 256)
+        else:
+            c._buf.fill_(fill)
+        O2, lse2 = attend(c, Q)
+        assert torch.equal(O, O2) and torch.equal(lse, lse2)
+        c.accumulate(Q, lse, prev=prev)
+        assert torch.equal(c.mass.view(torch.int32), mass.view(torch.int32))
+    check_attend(c, Q, O, lse, rows=np.array([0, rows - 1]))
+
+
+def test_evict_more_tokens_than_shared_memory_holds():
+    """200001 tokens of one head (a cluster keeps the keys of 131072 between its passes), and
+    a budget of none but ties."""
+    import torch
+    import kv_cache_compression_post_b200 as kvb
+    n, budget = 200001, 70000
+    c = kvb.Q8Cache(1, 64, 200064, 64, with_mass=True)
+    c.K.random_(0, 100)
+    c.V.random_(0, 100)
+    c.k_scale.fill_(0.5)
+    c.v_scale.fill_(0.25)
+    c.len.fill_(n)
+    to = kvb.Q8Cache(1, 64, 70016, 64)
+    kept = torch.empty(1, budget, dtype=torch.int32, device="cuda")
+    for mass in (torch.rand(200064, device="cuda"), torch.full((200064,), 3.0, device="cuda")):
+        c.mass[0] = mass
+        c.evict(to, budget, sink=11, recent=501, kept=kept)
+        w = mass[:n].clone()
+        w[:11] = w[n - 501:] = float("inf")
+        want = w.sort(descending=True, stable=True)[1][:budget].sort()[0]
+        assert torch.equal(kept[0].long(), want) and to.len.item() == budget
+        assert torch.equal(to.K[0, :budget], c.K[0, want]) and torch.equal(to.V[0, :budget], c.V[0, want])
+
+
+def test_attend_work_past_32_bits():
+    """A split whose costs times the CTAs pass 2^32: 80 heads, 24000 queries, 65536 tokens."""
+    import torch
+    import kv_cache_compression_post_b200 as kvb
+    H, rows, n = 80, 24000, 65536
+    c = kvb.Q8Cache(H, 64, n, 128, max_queries=rows)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(n, 64, generator=g, device="cuda")
+    c.K[:] = (64 * x).to(torch.float8_e4m3fn).view(torch.uint8)
+    c.V[:] = (64 * x.flip(0)).to(torch.float8_e4m3fn).view(torch.uint8)
+    c.k_scale.fill_(2.0 ** -6)
+    c.v_scale.fill_(2.0 ** -6)
+    c.len.fill_(n)
+    Q = torch.randn(1, rows, 64, generator=g, device="cuda").bfloat16().expand(H, -1, -1).contiguous()
+    O, lse = attend(c, Q)
+    assert c.status() == 0
+    assert torch.equal(lse.isfinite().sum(), torch.tensor(H * rows, device="cuda"))
+    one = kvb.Q8Cache(1, 64, n, 128, max_queries=rows)
+    for s, t in ((c.K, one.K), (c.V, one.V), (c.k_scale, one.k_scale), (c.v_scale, one.v_scale), (c.len, one.len)):
+        t.copy_(s[:1])
+    for h in (0, 41, H - 1):
+        check_attend(one, Q[h:h + 1], O[h:h + 1], lse[h:h + 1], rows=np.array([0, 11111, rows - 1]))
+    # the same inputs in every head: the same outputs, but for where a unit was cut
+    assert float((O.float() - O[:1].float()).abs().max()) <= 2.0 ** -7 * float(O[0].float().abs().max())
+
+
+def test_binding_refuses_wrong_tensors_and_devices():
+    import torch
+    import kv_cache_compression_post_b200 as kvb
+    H, d = 2, 64
+    c = kvb.Q8Cache(H, d, 128, 64, max_queries=4)
+    Q = torch.zeros(H, 4, d, device="cuda", dtype=torch.bfloat16)
+    O, lse = torch.empty_like(Q), torch.empty(H, 4, device="cuda")
+    bad = [lambda: c.attend(Q.float(), O, lse), lambda: c.attend(Q, O.float(), lse), lambda: c.attend(Q, O[:, :3], lse),
+           lambda: c.attend(Q.cpu(), O, lse), lambda: c.attend(Q, O, lse.double()), lambda: c.attend(Q, O, lse[:1]),
+           lambda: c.attend(Q[:1], O[:1], lse[:1]), lambda: c.attend(Q[..., ::2], O[..., ::2], lse),
+           lambda: c.attend(Q.transpose(0, 1).contiguous().transpose(0, 1), O, lse), lambda: c.attend(Q[0], O[0], lse[0]),
+           lambda: c.attend(Q[:, :0], O[:, :0], lse[:, :0]),
+           lambda: c.append(Q, Q[:, :2]), lambda: c.append(Q, Q.float()), lambda: c.append(Q[..., ::2], Q[..., ::2]),
+           lambda: c.append(Q, Q, start=torch.zeros(H, device="cuda")), lambda: c.append(Q.cpu(), Q.cpu()),
+           lambda: c.accumulate(Q, lse), lambda: c.evict(kvb.Q8Cache(H, d, 64, 64), 10),
+           lambda: kvb.Q8Cache(H, d, 100, 64), lambda: kvb.Q8Cache(H, 96, 128, 64), lambda: kvb.Q8Cache(H, d, 128, 64, K=O),
+           lambda: kvb.rope(Q, torch.zeros(4, 3, device="cuda"), O, (1, 1, 1)),
+           lambda: kvb.rope(Q, torch.zeros(4, 3, dtype=torch.int32), O, (1, 1, 1)),
+           lambda: kvb.rope(Q, torch.zeros(4, 3, dtype=torch.int32, device="cuda"), O, (30, 2, 1)),
+           lambda: kvb.rope(Q, torch.zeros(4, 3, dtype=torch.int32, device="cuda"), O, (1, 1))]
+    for i, f in enumerate(bad):
+        with pytest.raises(kvb.KvbError) as e:
+            f()
+        assert e.value.status in (1, 7), i
+    big = torch.zeros(H, 300, d, device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(kvb.KvbError) as e:               # more queries than the workspace is for
+        c.attend(big, big.clone())
+    assert e.value.status == 2
+    c.device = 1                                         # a cache of another device than the current one
+    with pytest.raises(kvb.KvbError) as e:
+        c.attend(Q, O, lse)
+    assert e.value.status == 1
