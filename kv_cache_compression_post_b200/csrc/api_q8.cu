@@ -205,7 +205,9 @@ kvb_status kvb_q8_evict(const kvb_q8_cache* src, const kvb_q8_cache* dst, int32_
   a.len = dst->len;
   a.to_mass = dst->mass;
   a.cap = dst->capacity;
-  a.budget = budget;
+  // the scratch list has a place per token of the source: a larger budget keeps them all
+  // and needs no more
+  a.budget = kept || budget < src->capacity ? budget : src->capacity;
   a.sink = sink;
   a.recent = recent;
   a.kept = kept ? kept : s.kept;

@@ -263,7 +263,8 @@ cudaError_t launch_q8_evict(const Q8EvictArgs& a, cudaStream_t st) {
   }
   if (e != cudaSuccess) return e;
   LaunchTrace trace("q8_gather_kernel", st);
-  const dim3 grid((a.budget + kGatherTok - 1) / kGatherTok, a.src.H);
+  const int most = a.budget < a.src.cap ? a.budget : a.src.cap;
+  const dim3 grid((most + kGatherTok - 1) / kGatherTok, a.src.H);
   return a.src.d == 128 ? launch_pdl(q8_gather_kernel<128>, grid, dim3(kGatherThreads), 0, st, a)
                         : launch_pdl(q8_gather_kernel<64>, grid, dim3(kGatherThreads), 0, st, a);
 }

@@ -625,6 +625,30 @@ def test_evict_more_tokens_than_shared_memory_holds():
         assert torch.equal(to.K[0, :budget], c.K[0, want]) and torch.equal(to.V[0, :budget], c.V[0, want])
 
 
+@pytest.mark.parametrize("listed", [False, True])
+def test_evict_into_a_larger_cache(listed):
+    """A budget above the source's capacity keeps all, and nothing behind the workspace or
+    the list is written."""
+    import torch
+    import kv_cache_compression_post_b200 as kvb
+    H, cap, budget = 64, 16, 65536
+    lens = [(7 * h) % (cap + 1) for h in range(H)]
+    c = filled(H, 64, cap, 16, "bf16", lens, 5)
+    to = kvb.Q8Cache(H, 64, budget, 16, with_mass=True)
+    kept = torch.full((H, budget), -5, dtype=torch.int32, device="cuda") if listed else None
+    buf = torch.full((c.nbytes + (32 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+    ws = (buf.data_ptr() + 255) & ~255
+    end = ws - buf.data_ptr() + c.nbytes
+    kvb.kvb_q8_evict(c.c, to.c, budget, 3, budget - 3, kept, ws, c.nbytes)
+    assert bool((buf[end:] == 0xA5).all())
+    assert to.len.tolist() == lens
+    for h, n in enumerate(lens):
+        assert torch.equal(to.K[h, :n], c.K[h, :n]) and torch.equal(to.V[h, :n], c.V[h, :n])
+        assert torch.equal(to.mass[h, :n], c.mass[h, :n])
+        if listed:
+            assert kept[h, :n].tolist() == list(range(n)) and bool((kept[h, n:] == -5).all())
+
+
 def test_attend_work_past_32_bits():
     """A split whose costs times the CTAs pass 2^32: 80 heads, 24000 queries, 65536 tokens."""
     import torch
