@@ -415,7 +415,8 @@ KVB_API kvb_status kvb_segment_cosine(const void* K, const void* nextK, int32_t 
  * X, out: device, rows of head_dim contiguous elements; element (h, t) starts
  *   h * head_stride + t * token_stride elements from the pointer, so the
  *   projection's [N][H][d] is turned head-major ([H][N][d]) in the same pass.
- *   out may equal X with equal strides; otherwise the two must not overlap.
+ *   out may equal X with equal strides; otherwise the two must not overlap, nor out's
+ *   rows one another (a stride of 0 over several rows is KVB_E_INVAL; X's may be 0).
  * pos: device int32 [n_tokens][3].  axis_pairs: host int32[3], each >= 0, their
  *   sum <= head_dim / 2.  base > 0, finite.  heads 1..65535, n_tokens >= 0,
  *   head_dim a multiple of 8 up to 256.

@@ -218,6 +218,7 @@ extern "C" kvb_status kvb_rope(const void* X, const int32_t* pos, int32_t heads,
   const int64_t unit = dtype == KVB_BF16 ? 8 : 4;  // elements of 16 bytes
   if (x_head_stride % unit || x_token_stride % unit || out_head_stride % unit || out_token_stride % unit)
     return KVB_E_INVAL;
+  if ((heads > 1 && out_head_stride == 0) || (n_tokens > 1 && out_token_stride == 0)) return KVB_E_INVAL;
   if (X == out && (x_head_stride != out_head_stride || x_token_stride != out_token_stride)) return KVB_E_INVAL;
   DeviceInfo dev;
   if (!current_device(&dev)) return KVB_E_CUDA;
@@ -235,9 +236,9 @@ extern "C" kvb_status kvb_rope(const void* X, const int32_t* pos, int32_t heads,
   a.xt = x_token_stride;
   a.oh = out_head_stride;
   a.ot = out_token_stride;
-  const int tiles = (n_tokens + kTok - 1) / kTok;
+  const int tiles = (n_tokens - 1) / kTok + 1;
   // all heads of a token share its angles; few tokens spread their heads over CTAs
-  const int want = (4 * dev.n_sm + tiles - 1) / tiles;
+  const int want = (4 * dev.n_sm - 1) / tiles + 1;
   const int split = want < heads ? (want < 1 ? 1 : want) : heads;
   a.heads_per_cta = (heads + split - 1) / split;
   const dim3 grid(tiles, (heads + a.heads_per_cta - 1) / a.heads_per_cta);

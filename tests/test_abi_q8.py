@@ -141,7 +141,8 @@ def test_rope_refusals():
                dict(pairs=(-1, 2, 2)), dict(pairs=(12, 11, 10)), dict(pairs=(2 ** 31 - 1, 2 ** 31 - 1, 2)),
                dict(base=0.0), dict(base=-2.0), dict(base=nan), dict(base=float("inf")), dict(pairing=2),
                dict(xs=(324, 64)), dict(xs=(320, 68)), dict(os=(322, 64)), dict(os=(320, 66)),
-               dict(xs=(64, 128), os=(320, 64))]:                # in place with other strides
+               dict(xs=(64, 128), os=(320, 64)),                 # in place with other strides
+               dict(os=(0, 64)), dict(os=(320, 0)), dict(os=(0, 0))]:        # rows of out on one another
         assert f(**kw) == 1, kw
     assert f(n=0) == 0
 
