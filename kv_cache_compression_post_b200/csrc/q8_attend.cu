@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const __grid_con
         float alpha = 1.f, rs = 0.f;
         bool moved = false;
         if (j == pc.j0) {
-          m = mt;
+          m = fmaxf(mt, -3e38f);  // scores past fp32's range are -inf, and weigh 0 against any m
         } else if (mt > m + kRescale) {
           alpha = ex2_approx(m - mt);
           m = mt;

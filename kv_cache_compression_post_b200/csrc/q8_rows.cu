@@ -14,7 +14,7 @@
 // fp16 11, so nothing is lost above 2^-14 of the row's largest).
 // What bounds it: widening a pair of codes takes 8 clk of a scheduler's ALU, ~1000 of the
 // ~1500 clk of a 32-token step, beside which the memory would need ~1400 (8 heads, 8 rows,
-// 98304 tokens on average: 41 us of memory alone, 40 us of arithmetic alone, 50 us
+// 102400 tokens on average: 41 us of memory alone, 40 us of arithmetic alone, 50 us
 // together, and the merge).  E4M3 operands of mma.sync do not help, they are widened in
 // the same way (same time, measured).
 //
@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(kF32Threads) q8_attend_f32_kernel(const Q8Atte
 #pragma unroll
           for (int k = 0; k < D / 8; ++k) acc[r][k] *= al;
         }
-        const float p = key < end ? exp2f(x - m[r]) : 0.f;
+        const float p = x == -INFINITY ? 0.f : exp2f(x - m[r]);  // behind the end, or past fp32's range
         l[r] += p;
         const float pv = p * vs;
 #pragma unroll

@@ -238,6 +238,47 @@ def test_attend_non_finite_queries_stay_in_their_row(rows, dtype):
     assert torch.equal(O[keep], clean[keep]) and torch.equal(lse[keep], clean_lse[keep])
 
 
+@pytest.mark.parametrize("dtype,rows", [("bf16", 1), ("bf16", 20), ("bf16", 70), ("f32", 3)])
+def test_attend_scores_past_the_range_of_floats(rows, dtype):
+    """The first 300 tokens' scores lie below -2^128 and count as -inf: they weigh nothing,
+    and nothing else is touched."""
+    import torch
+    H, d, n, bad = 2, 128, 700, 300
+    torch.manual_seed(rows)
+    dt = _dt(dtype)[0]
+    c = poisoned(H, d, 1024, 16, dtype, max_queries=rows)
+    K, V = torch.randn(H, n, d, device="cuda"), torch.randn(H, n, d, device="cuda")
+    K[:, :, 0] = 0.0
+    K[:, :bad] = 0.0
+    K[:, :bad, 0] = -2.0 ** 126
+    c.append(K[:, :304].to(dt), V[:, :304].to(dt))
+    c.append(K[:, 304:].to(dt), V[:, 304:].to(dt))
+    Q = torch.randn(H, rows, d, device="cuda").to(dt)
+    Q[:, :, 0] = 64.0
+    O, lse = attend(c, Q)
+    assert c.status() == 0
+    # what is left: a cache without those tokens (300 = 18 blocks and 12 tokens; the four
+    # that share a block with them lose their codes to its scale, and stay)
+    one = poisoned(H, d, 1024, 16, dtype, max_queries=rows)
+    for s, t in ((c.K, one.K), (c.V, one.V)):
+        t[:, :n - 288] = s[:, 288:n]
+    for s, t in ((c.k_scale, one.k_scale), (c.v_scale, one.v_scale)):
+        t[:, :64 - 18] = s[:, 18:]
+    one.len.fill_(n - 288)
+    for h in range(H):
+        Kh, Vh = head_values(one, h)
+        assert np.all(Kh[:12, 0] == -2.0 ** 126) and np.all(Kh[12:16] == 0)
+        q = Q[h].double().cpu().numpy()
+        ref, ref_lse, size = q8.attend(q, Kh[12:], Vh[12:], 1.0 / np.sqrt(d))
+        dS = (np.abs(q) @ np.abs(Kh[12:]).T).max(1, keepdims=True) / np.sqrt(d) * 2.0 ** -17
+        rel = 4 * dS + 2.0 ** -11 + 2.0 ** -18
+        half = torch.finfo(dt).eps / 2
+        tol = rel * size + half * (np.abs(ref) + rel * size)
+        assert np.all(np.abs(O[h].double().cpu().numpy() - ref) <= tol)
+        tl = dS[:, 0] + 2.0 ** -18 + 2.0 ** -17 * (1 + np.abs(ref_lse))
+        assert np.all(np.abs(lse[h].double().cpu().numpy() - ref_lse) <= tl)
+
+
 def test_attend_lengths_out_of_range_and_poison():
     """A length past the capacity is the capacity, a negative one 0; nothing behind a
     length is read as a value (it is NaN here), rows behind stay as they were."""
