@@ -82,17 +82,6 @@ struct Args {
   unsigned int* cnt;   // [H][npair][2] arrivals, zeroed by the split kernel
 };
 
-// D[tmem] (+)= A[smem] * B[smem]^T, kind::f8f6f4 (E4M3 here), 32 channels per instruction
-__device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                          uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // --------------------------------------------------------------- query parts
 // One warp per row: hi, lo codes and the row's coefficient.  Also zeroes the arrival
 // counters of the launch that follows.

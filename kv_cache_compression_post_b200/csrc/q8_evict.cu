@@ -8,9 +8,9 @@
 // the lower positions stay.  Bound by latency: a head has one answer per pass to wait for
 // (one CTA per head took 150 us for 8 heads of 131072 tokens).
 // q8_gather_kernel, one CTA per 128 tokens of the result: reads and writes each kept row
-// once, every word of its rows in flight at once.  The result's block takes the largest scale among its tokens;
-// rows from blocks of smaller scale are rounded anew (exactly scaled where both are
-// powers of two), others are copied bit for bit.
+// once, every word of its rows in flight at once.  The result's block takes the largest
+// scale among its tokens; rows from blocks of smaller scale are rounded anew (exactly
+// scaled where both are powers of two), others are copied bit for bit.
 #include <cooperative_groups.h>
 
 #include "host_util.h"

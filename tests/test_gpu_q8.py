@@ -386,6 +386,17 @@ def test_mass_matches_oracle(d, block, rows, dtype):
 
 
 # ------------------------------------------------------------------ eviction
+@pytest.mark.parametrize("rows,dtype", [(1, "bf16"), (20, "bf16"), (300, "bf16"), (1, "f32"), (5, "f32")])
+def test_mass_of_rows_that_saw_nothing(rows, dtype):
+    """Rows of lse -inf weigh nothing: what was there before stays to the bit."""
+    import torch
+    c = filled(2, 128, 512, 64, dtype, [500, 0], rows, max_queries=rows)
+    prev = torch.rand(2, 512, device="cuda") * 2.0 ** -110
+    Q = torch.randn(2, rows, 128, device="cuda").to(_dt(dtype)[0])
+    c.accumulate(Q, torch.full((2, rows), float("-inf"), device="cuda"), prev=prev)
+    assert torch.equal(c.mass[0, :500], prev[0, :500])
+
+
 @pytest.mark.parametrize("d,block", [(64, 16), (128, 64), (128, 128)])
 @pytest.mark.parametrize("budget,sink,recent", [(1, 0, 0), (100, 0, 0), (100, 7, 30), (100, 40, 60), (300, 1, 299),
                                                 (333, 16, 64), (2000, 5, 5)])
