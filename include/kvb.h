@@ -477,7 +477,9 @@ typedef struct {
 KVB_API size_t kvb_q8_workspace_size(const kvb_q8_cache* c, int32_t max_queries, kvb_dtype dtype);
 
 /* Append n tokens to every head: token i of head h is written at start[h] + i and
- * len[h] becomes start[h] + n (start NULL: the present len).  K and V are rows of d
+ * len[h] becomes start[h] + n (start NULL: the present len; start may be len, and does
+ * not overlap it otherwise, KVB_E_INVAL).  Tokens between len[h] and a start above it
+ * are taken as the arrays hold them, their blocks' scales too.  K and V are rows of d
  * contiguous elements of `dtype`; row (h, i) starts h * head_stride + i *
  * token_stride elements from its pointer (pointers and strides multiples of 16
  * bytes, else KVB_E_INVAL).  A block that already holds tokens before start[h]

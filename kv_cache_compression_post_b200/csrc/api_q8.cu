@@ -101,6 +101,11 @@ kvb_status kvb_q8_append(const kvb_q8_cache* c, const void* K, int64_t k_head_st
   if (ok != KVB_OK) return ok;
   if (n < 0 || !dtype_ok(dtype) || !aligned(start, 4)) return KVB_E_INVAL;
   if (n > c->capacity) return KVB_E_INVAL;
+  if (start && start != c->len) {
+    // a length moved for one head must not be another's start
+    const uintptr_t s = reinterpret_cast<uintptr_t>(start), l = reinterpret_cast<uintptr_t>(c->len), b = 4u * c->heads;
+    if (s < l + b && l < s + b) return KVB_E_INVAL;
+  }
   if (n == 0 && !start) return KVB_OK;
   if (n > 0 && (!K || !V)) return KVB_E_INVAL;
   const int64_t unit = dtype == KVB_BF16 ? 8 : 4;

@@ -84,6 +84,8 @@ def test_append_refusals():
         assert f(c, P, s[0], s[1], P, s[2], s[3], 4, 0, None, None) == 1     # bf16 rows 8 bytes off
         assert f(c, P, s[0] + 2, s[1], P, s[2] + 2, s[3] + 2, 4, 1, None, None) == 1
     assert f(c, P, 128, 128, P, 128, 128, 4, 0, ctypes.c_void_p(0x5002), None) == 1
+    for at in (0x5004, 0x4FFC):                                              # another head's length for a start
+        assert f(c, P, 128, 128, P, 128, 128, 4, 0, ctypes.c_void_p(at), None) == 1
     assert f(c, None, 0, 0, None, 0, 0, 0, 0, None, None) == 0               # nothing to do
 
 

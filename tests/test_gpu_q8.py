@@ -163,6 +163,28 @@ def test_append_start_room_and_lengths():
         assert c.len.tolist() == [9] * H    # a length set back
 
 
+@pytest.mark.parametrize("n", [3, 200])
+def test_append_start_is_the_length(n):
+    """start None, the length's own array and a copy of it are one call, room or no room, also
+    behind one another."""
+    import torch
+    H, d, cap, block = 40, 64, 512, 16
+    lens = [(37 * h) % 120 for h in range(H)]
+    lens[3] = 480
+    caches = [filled(H, d, cap, block, "bf16", lens, 9) for _ in range(3)]
+    for _ in range(2):
+        K, V = torch.randn(2, H, n, d, device="cuda").bfloat16()
+        for c, start in zip(caches, (None, caches[1].len, caches[2].len.clone())):
+            c.append(K, V, start=start)
+    a = caches[0]
+    room = [x + 2 * n <= cap for x in lens]
+    assert a.len.tolist() == [x + 2 * n if r else x + n if x + n <= cap else x for x, r in zip(lens, room)]
+    for b in caches[1:]:
+        assert b.status() == a.status() == (0 if all(room) else 5)
+        for x, y in zip((a.K, a.V, a.k_scale, a.v_scale, a.mass, a.len), (b.K, b.V, b.k_scale, b.v_scale, b.mass, b.len)):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
 # ------------------------------------------------------------------ attention
 LENS = [0, 1, 15, 16, 17, 31, 63, 64, 65, 127, 128, 129, 500]
 
