@@ -4,7 +4,6 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -31,18 +30,38 @@ struct Q8View {
 
 __device__ __forceinline__ int q8_len(const int* len, int h, int cap) { return min(max(len[h], 0), cap); }
 
-// two E4M3 codes (low 16 bits) -> two fp16 (exact)
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t c) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c & 0xFFFFu), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+// four E4M3 codes -> four fp16 (exact).  In PTX, on the halves of the word: the two
+// conversions take 5 clk of a warp's ALU; through the header's conversion of a 16-bit
+// storage type, which goes by way of two 16-bit fields, they took 15.
+struct F16x4 {
+  uint32_t lo, hi;
+};
+__device__ __forceinline__ F16x4 e4m3x4_to_f16x4(uint32_t c) {
+  F16x4 r;
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(r.lo), "=r"(r.hi)
+      : "r"(c));
+  return r;
 }
-__device__ __forceinline__ float2 e4m3x2_to_f32x2(uint32_t c) {
-  const uint32_t h = e4m3x2_to_f16x2(c);
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+__device__ __forceinline__ float2 f16x2_to_f32x2(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2*>(&h)); }
+__device__ __forceinline__ float4 e4m3x4_to_f32x4(uint32_t c) {
+  const F16x4 h = e4m3x4_to_f16x4(c);
+  const float2 a = f16x2_to_f32x2(h.lo), b = f16x2_to_f32x2(h.hi);
+  return make_float4(a.x, a.y, b.x, b.y);
 }
-// two floats -> two E4M3 codes, to nearest even, saturating
-__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
-  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3));
+// four floats -> four E4M3 codes, to nearest even, saturating
+__device__ __forceinline__ uint32_t f32x4_to_e4m3x4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+      "mov.b32 %0, {l, h};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);

@@ -50,8 +50,8 @@ struct Words<float> {
 };
 
 __device__ __forceinline__ uint2 codes8(const float (&f)[8], float inv) {
-  return make_uint2(f32x2_to_e4m3x2(f[0] * inv, f[1] * inv) | (f32x2_to_e4m3x2(f[2] * inv, f[3] * inv) << 16),
-                    f32x2_to_e4m3x2(f[4] * inv, f[5] * inv) | (f32x2_to_e4m3x2(f[6] * inv, f[7] * inv) << 16));
+  return make_uint2(f32x4_to_e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
+                    f32x4_to_e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
 }
 
 // One (block b, head h, kv) by kHalf threads; `bar`: their named barrier, `s_max`: 8
@@ -112,9 +112,8 @@ __device__ __forceinline__ void append_block(const Q8AppendArgs& a, int kv, int 
     for (int i = tid; i < old * per; i += kHalf) {
       uint2* p = reinterpret_cast<uint2*>(code + (static_cast<size_t>(b) * a.block * per + i) * 8);
       const uint2 c = *p;
-      const float2 x = e4m3x2_to_f32x2(c.x), y = e4m3x2_to_f32x2(c.x >> 16), z = e4m3x2_to_f32x2(c.y),
-                   v = e4m3x2_to_f32x2(c.y >> 16);
-      const float f[8] = {x.x, x.y, y.x, y.y, z.x, z.y, v.x, v.y};
+      const float4 x = e4m3x4_to_f32x4(c.x), y = e4m3x4_to_f32x4(c.y);
+      const float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
       *p = codes8(f, shrink);
     }
   }

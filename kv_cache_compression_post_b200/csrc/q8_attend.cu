@@ -123,15 +123,16 @@ __global__ void __launch_bounds__(256) q8_split_q_kernel(const __nv_bfloat16* Q,
       for (int o = kLanes / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       const int e = max(exponent_of(mx), -100) - 7;  // mx 2^-e in [2^7, 2^8)
       const float down = pow2f(-e);
-      uint32_t h[2] = {0u, 0u}, l[2] = {0u, 0u};
+      uint32_t h[2], l[2];
 #pragma unroll
-      for (int k = 0; k < 8; k += 2) {
+      for (int k = 0; k < 2; ++k) {
         // an infinite element becomes a NaN: its row is NaN, as its scores would be
-        const float x = fabsf(f[k]) <= 3.4e38f ? f[k] * down : NAN, y = fabsf(f[k + 1]) <= 3.4e38f ? f[k + 1] * down : NAN;
-        const uint32_t code = f32x2_to_e4m3x2(x, y);
-        const float2 b = e4m3x2_to_f32x2(code);
-        h[k / 4] |= code << (8 * (k & 3));
-        l[k / 4] |= f32x2_to_e4m3x2(x - b.x, y - b.y) << (8 * (k & 3));
+        float x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = fabsf(f[4 * k + i]) <= 3.4e38f ? f[4 * k + i] * down : NAN;
+        h[k] = f32x4_to_e4m3x4(x[0], x[1], x[2], x[3]);
+        const float4 b = e4m3x4_to_f32x4(h[k]);
+        l[k] = f32x4_to_e4m3x4(x[0] - b.x, x[1] - b.y, x[2] - b.z, x[3] - b.w);
       }
       if (row >= rows) continue;
       reinterpret_cast<uint2*>(hi + row * D)[c] = make_uint2(h[0], h[1]);
@@ -412,9 +413,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const __grid_con
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             if ((b + i) * kStep >= nv) c[i] = make_uint2(0u, 0u);
-            *reinterpret_cast<uint4*>(dst + (b + i) * kStep * 128) =
-                make_uint4(e4m3x2_to_f16x2(c[i].x), e4m3x2_to_f16x2(c[i].x >> 16), e4m3x2_to_f16x2(c[i].y),
-                           e4m3x2_to_f16x2(c[i].y >> 16));
+            const F16x4 x = e4m3x4_to_f16x4(c[i].x), y = e4m3x4_to_f16x4(c[i].y);
+            *reinterpret_cast<uint4*>(dst + (b + i) * kStep * 128) = make_uint4(x.lo, x.hi, y.lo, y.hi);
           }
         }
         fence_proxy_async_smem();

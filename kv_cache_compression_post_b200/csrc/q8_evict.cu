@@ -191,8 +191,8 @@ constexpr int kGatherTok = 128;  // tokens of the result per CTA: one to eight b
 
 // four codes times r, rounded to E4M3
 __device__ __forceinline__ uint32_t rescale4(uint32_t c, float r) {
-  const float2 x = e4m3x2_to_f32x2(c), y = e4m3x2_to_f32x2(c >> 16);
-  return f32x2_to_e4m3x2(x.x * r, x.y * r) | (f32x2_to_e4m3x2(y.x * r, y.y * r) << 16);
+  const float4 x = e4m3x4_to_f32x4(c);
+  return f32x4_to_e4m3x4(x.x * r, x.y * r, x.z * r, x.w * r);
 }
 
 template <int D>

@@ -179,7 +179,10 @@ struct KWords {
       for (int hb = 0; hb < D / 64; ++hb) {
         const uint32_t u[4] = {w[j][hb].x, w[j][hb].y, w[j][hb].z, w[j][hb].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) q.step(s[j], hb * 4 + i, e4m3x2_to_f16x2(u[i]), e4m3x2_to_f16x2(u[i] >> 16));
+        for (int i = 0; i < 4; ++i) {
+          const F16x4 k4 = e4m3x4_to_f16x4(u[i]);
+          q.step(s[j], hb * 4 + i, k4.lo, k4.hi);
+        }
       }
     }
   }
@@ -211,10 +214,11 @@ struct VWords {
     for (int q = 0; q < kW; ++q) {
       const uint32_t a0 = __byte_perm(w[u][0][q], w[u][1][q], 0x5140), a1 = __byte_perm(w[u][0][q], w[u][1][q], 0x7362);
       const uint32_t b0 = __byte_perm(w[u][2][q], w[u][3][q], 0x5140), b1 = __byte_perm(w[u][2][q], w[u][3][q], 0x7362);
-      mma_16816(o[4 * q + 0], p, e4m3x2_to_f16x2(a0), e4m3x2_to_f16x2(b0));
-      mma_16816(o[4 * q + 1], p, e4m3x2_to_f16x2(a0 >> 16), e4m3x2_to_f16x2(b0 >> 16));
-      mma_16816(o[4 * q + 2], p, e4m3x2_to_f16x2(a1), e4m3x2_to_f16x2(b1));
-      mma_16816(o[4 * q + 3], p, e4m3x2_to_f16x2(a1 >> 16), e4m3x2_to_f16x2(b1 >> 16));
+      const F16x4 x0 = e4m3x4_to_f16x4(a0), y0 = e4m3x4_to_f16x4(b0), x1 = e4m3x4_to_f16x4(a1), y1 = e4m3x4_to_f16x4(b1);
+      mma_16816(o[4 * q + 0], p, x0.lo, y0.lo);
+      mma_16816(o[4 * q + 1], p, x0.hi, y0.hi);
+      mma_16816(o[4 * q + 2], p, x1.lo, y1.lo);
+      mma_16816(o[4 * q + 3], p, x1.hi, y1.hi);
     }
   }
 };
@@ -560,8 +564,8 @@ __device__ __forceinline__ void load_codes(const uint8_t* p, float (&f)[D / 8]) 
   }
 #pragma unroll
   for (int k = 0; k < D / 32; ++k) {
-    const float2 a = e4m3x2_to_f32x2(w[k]), b = e4m3x2_to_f32x2(w[k] >> 16);
-    f[4 * k] = a.x, f[4 * k + 1] = a.y, f[4 * k + 2] = b.x, f[4 * k + 3] = b.y;
+    const float4 x = e4m3x4_to_f32x4(w[k]);
+    f[4 * k] = x.x, f[4 * k + 1] = x.y, f[4 * k + 2] = x.z, f[4 * k + 3] = x.w;
   }
 }
 template <int D>
