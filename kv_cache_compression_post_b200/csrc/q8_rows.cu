@@ -32,14 +32,15 @@ using namespace sm100;
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;  // ten or twelve warps, with their registers cut to fit, were slower
+constexpr int kThreads = 256;  // of the weights' kernels
+constexpr int kWarps = kThreads / 32;
+constexpr int kRowsThreads = 256;      // ten or twelve warps, with their registers cut to fit, were slower
+constexpr int kFewThreads = 256;
 constexpr int kRing = 2;               // stages of a warp's ring (three: 5 % slower)
 constexpr int kTile = 64;    // tokens per key tile of the split
 constexpr int kSub = 32;     // tokens a warp takes at a time
 constexpr int kRows = 16;    // rows per row tile
-constexpr float kPBias = 8.f;
-constexpr int kMinTiles = 4;  // a CTA's share: one 32-token step for each warp
+constexpr int kMinTiles = 4;  // of a CTA of the f32 kernel
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -57,12 +58,12 @@ __device__ __forceinline__ float quad_sum(float v) {
   return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
 
-// The A fragments of one 16-row tile: row g and, unless FEW (at most eight rows), g + 8 of
-// this lane, channels 64 hb + 16 t .. + 15 in the order the K bytes come.  coef[i]: what
-// turns a raw dot product of row g + 8 i into log2 units (but for the token's scale).
-template <int D, bool FEW>
+// Query fragments: row g and, of a 16-row tile (I 2), g + 8 of this lane, channels
+// 64 hb + 16 t .. + 15 in the order the K bytes come.  coef[i]: what turns a raw dot
+// product of row g + 8 i into log2 units (but for the token's scale).
+template <int D, int I>
 struct QFrag {
-  static constexpr int kI = FEW ? 1 : 2;
+  static constexpr int kI = I;
   uint32_t a[D / 16][2 * kI];  // [16-channel step][(half of the step) * kI + row]
   float coef[kI];
   uint4 raw[kI][D / 32];
@@ -109,10 +110,6 @@ struct QFrag {
         }
       }
     }
-  }
-  __device__ __forceinline__ void step(float (&c)[4], int k, uint32_t b0, uint32_t b1) const {
-    const uint32_t r[4] = {a[k][0], FEW ? 0u : a[k][1], a[k][kI], FEW ? 0u : a[k][2 * kI - 1]};
-    mma_16816(c, r, b0, b1);
   }
 };
 
@@ -167,10 +164,8 @@ struct KWords {
         w[j][hb] = __ldg(reinterpret_cast<const uint4*>(K + static_cast<size_t>(key) * D + hb * 64 + t * 16));
     }
   }
-  // s[j]: raw dot products of rows g (0, 1) and, unless FEW, g + 8 (2, 3) with tokens
-  // 8 j + 2 t, + 1
-  template <bool FEW>
-  __device__ __forceinline__ void dots(const QFrag<D, FEW>& q, float (&s)[4][4]) const {
+  // s[j]: raw dot products of rows g (0, 1) and g + 8 (2, 3) with tokens 8 j + 2 t, + 1
+  __device__ __forceinline__ void dots(const QFrag<D, 2>& q, float (&s)[4][4]) const {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
 #pragma unroll
@@ -181,9 +176,33 @@ struct KWords {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const F16x4 k4 = e4m3x4_to_f16x4(u[i]);
-          q.step(s[j], hb * 4 + i, k4.lo, k4.hi);
+          mma_16816(s[j], q.a[hb * 4 + i], k4.lo, k4.hi);
         }
       }
+    }
+  }
+  // at most eight rows: the tokens are the product's 16 rows and the queries its 8 columns,
+  // half the instructions.  s[u]: tokens 16 u + g (0, 1) and 16 u + g + 8 (2, 3) with rows
+  // 2 t, + 1.  Two chains of products each, so that they do not wait on one another.
+  __device__ __forceinline__ void dots_few(const QFrag<D, 1>& q, float (&s)[2][4]) const {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      float c[2][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) c[0][k] = c[1][k] = 0.f;
+#pragma unroll
+      for (int hb = 0; hb < D / 64; ++hb) {
+        const uint4 &x = w[2 * u][hb], &y = w[2 * u + 1][hb];
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const F16x4 x4 = e4m3x4_to_f16x4(xs[i]), y4 = e4m3x4_to_f16x4(ys[i]);
+          const uint32_t a[4] = {x4.lo, y4.lo, x4.hi, y4.hi};
+          mma_16816(c[i & 1], a, q.a[hb * 4 + i][0], q.a[hb * 4 + i][1]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[u][k] = c[0][k] + c[1][k];
     }
   }
 };
@@ -221,16 +240,216 @@ struct VWords {
       mma_16816(o[4 * q + 3], p, x1.hi, y1.hi);
     }
   }
+  // at most eight rows: channels are the product's rows.  o[2 q + j]: channels (D / 8) g +
+  // 4 q + 2 j (0, 1) and the next (2, 3) of rows 2 t, + 1; p: row g, tokens 2 t, + 1 and + 8
+  __device__ __forceinline__ void accumulate_few(int u, uint32_t p0, uint32_t p1, float (&o)[D / 16][4]) const {
+#pragma unroll
+    for (int q = 0; q < kW; ++q) {
+      const uint32_t a0 = __byte_perm(w[u][0][q], w[u][1][q], 0x5140), a1 = __byte_perm(w[u][0][q], w[u][1][q], 0x7362);
+      const uint32_t b0 = __byte_perm(w[u][2][q], w[u][3][q], 0x5140), b1 = __byte_perm(w[u][2][q], w[u][3][q], 0x7362);
+      const F16x4 x0 = e4m3x4_to_f16x4(a0), y0 = e4m3x4_to_f16x4(b0), x1 = e4m3x4_to_f16x4(a1), y1 = e4m3x4_to_f16x4(b1);
+      const uint32_t f0[4] = {x0.lo, x0.hi, y0.lo, y0.hi}, f1[4] = {x1.lo, x1.hi, y1.lo, y1.hi};
+      mma_16816(o[2 * q], f0, p0, p1);
+      mma_16816(o[2 * q + 1], f1, p0, p1);
+    }
+  }
 };
+
+// 8 x 8 of 16 bits: lane (g, t) gives row g, columns 2 t, + 1 and receives those of the transpose
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
 
 template <int D>
 constexpr size_t slot_floats() { return static_cast<size_t>(kRows) * D + 2 * kRows; }
 
-// what the eight warps of a CTA leave for their merge
-template <int D>
+// what the warps of a CTA leave for their merge
+template <int D, int WARPS, int ROWS>
 struct RowsShared {
-  float o[kWarps][kRows][D + 4];
-  float m[kWarps][kRows], l[kWarps][kRows];
+  float o[WARPS][ROWS][D + 4];
+  float m[WARPS][ROWS], l[WARPS][ROWS];
+};
+
+// The scales of 32 tokens' two halves: K's, log2 and reciprocal of V's
+struct StepScales {
+  float kf[2], lv[2], iv[2];
+};
+
+// A warp's running softmax and outputs of up to 16 rows.
+template <int D>
+struct RowsAcc {
+  static constexpr int kTileRows = 16, kThreads = kRowsThreads, kWarps = kThreads / 32;
+  static constexpr float kBias = 8.f;
+  using Shared = RowsShared<D, kWarps, kTileRows>;
+  QFrag<D, 2> q;
+  float o[D / 8][4];
+  float m[2], l[2];  // rows g, g + 8
+
+  __device__ __forceinline__ void begin(float scale, int) {
+    q.widen(scale);
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[j][k] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) m[i] = -INFINITY, l[i] = 0.f;
+  }
+  __device__ __forceinline__ void step(const KWords<D>& kw, const uint8_t* v_stage, const StepScales& sc, int kb, int end,
+                                       int g, int t) {
+    float s[4][4];
+    kw.dots(q, s);
+    float mt[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int key = kb + 8 * j + 2 * t + (k & 1);
+        const float x = fmaf(s[j][k], q.coef[k >> 1] * sc.kf[j >> 1], sc.lv[j >> 1]);
+        s[j][k] = key < end ? x : -INFINITY;
+        mt[k >> 1] = fmaxf(mt[k >> 1], s[j][k]);
+      }
+    bool moved = false;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      mt[i] = quad_max(mt[i]);
+      moved |= mt[i] > m[i];
+    }
+    if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float mn = fmaxf(m[i], mt[i]);
+        const float al = mn == -INFINITY ? 1.f : exp2f(m[i] - mn);
+        m[i] = mn;
+        l[i] *= al;
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) {
+          o[j][2 * i] *= al;
+          o[j][2 * i + 1] *= al;
+        }
+      }
+    }
+    VWords<D> vw;
+    vw.load(v_stage, g, t);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint32_t p[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        // a row whose every score is -inf so far (NaN queries aside) keeps P = 0
+        const float b = (m[i] == -INFINITY ? 0.f : -m[i]) + kBias;
+        float r = 0.f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float x = ex2_approx(s[2 * u + j][2 * i] + b), y = ex2_approx(s[2 * u + j][2 * i + 1] + b);
+          r += x + y;
+          p[2 * j + i] = pack_f16x2(x, y);
+        }
+        l[i] = fmaf(r, sc.iv[u], l[i]);
+      }
+      vw.accumulate(u, p, o);
+    }
+  }
+  __device__ __forceinline__ void leave(Shared& sh, int warp, int rows, int g, int t) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) l[i] = quad_sum(l[i]);
+    if (t == 0) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) sh.m[warp][g + 8 * i] = m[i], sh.l[warp][g + 8 * i] = l[i];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int row = g + 8 * (k >> 1);
+      if (row >= rows) continue;
+      float* to = &sh.o[warp][row][(2 * t + (k & 1)) * (D / 8)];
+#pragma unroll
+      for (int j = 0; j < D / 8; j += 4)
+        *reinterpret_cast<float4*>(to + j) = make_float4(o[j][k], o[j + 1][k], o[j + 2][k], o[j + 3][k]);
+    }
+  }
+};
+
+// Of up to eight: rows 2 t, 2 t + 1 of this lane.  The maximum moves only when a score
+// passes it by kLag, which a vote finds without reducing over the lanes.
+template <int D>
+struct FewAcc {
+  static constexpr int kTileRows = 8, kThreads = kFewThreads, kWarps = kThreads / 32;
+  static constexpr float kBias = 6.f, kLag = 8.f;  // P <= 2^(kBias + kLag) < 65504
+  using Shared = RowsShared<D, kWarps, kTileRows>;
+  QFrag<D, 1> q;
+  float o[D / 16][4];
+  float coef[2], m[2], l[2];
+
+  __device__ __forceinline__ void begin(float scale, int t) {
+    q.widen(scale);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      coef[r] = __shfl_sync(0xffffffffu, q.coef[0], 4 * (2 * t + r));
+      m[r] = -INFINITY, l[r] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[j][k] = 0.f;
+  }
+  __device__ __forceinline__ void step(const KWords<D>& kw, const uint8_t* v_stage, const StepScales& sc, int kb, int end,
+                                       int g, int t) {
+    float s[2][4];
+    kw.dots_few(q, s);
+    float mt[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int key = kb + 16 * u + 8 * (k >> 1) + g;
+        const float x = fmaf(s[u][k], coef[k & 1] * sc.kf[u], sc.lv[u]);
+        s[u][k] = key < end ? x : -INFINITY;
+        mt[k & 1] = fmaxf(mt[k & 1], s[u][k]);
+      }
+    if (__any_sync(0xffffffffu, mt[0] > m[0] + kLag || mt[1] > m[1] + kLag)) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+#pragma unroll
+        for (int k = 4; k < 32; k <<= 1) mt[r] = fmaxf(mt[r], __shfl_xor_sync(0xffffffffu, mt[r], k));
+        const float mn = fmaxf(m[r], mt[r]);
+        const float al = mn == -INFINITY ? 1.f : exp2f(m[r] - mn);
+        m[r] = mn;
+        l[r] *= al;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          o[j][r] *= al;
+          o[j][2 + r] *= al;
+        }
+      }
+    }
+    VWords<D> vw;
+    vw.load(v_stage, g, t);
+    // a row whose every score is -inf so far (NaN queries aside) keeps P = 0
+    const float b0 = (m[0] == -INFINITY ? 0.f : -m[0]) + kBias, b1 = (m[1] == -INFINITY ? 0.f : -m[1]) + kBias;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const float x0 = ex2_approx(s[u][0] + b0), x1 = ex2_approx(s[u][1] + b1);
+      const float y0 = ex2_approx(s[u][2] + b0), y1 = ex2_approx(s[u][3] + b1);
+      l[0] = fmaf(x0 + y0, sc.iv[u], l[0]);
+      l[1] = fmaf(x1 + y1, sc.iv[u], l[1]);
+      vw.accumulate_few(u, transpose8(pack_f16x2(x0, x1)), transpose8(pack_f16x2(y0, y1)), o);
+    }
+  }
+  __device__ __forceinline__ void leave(Shared& sh, int warp, int rows, int g, int t) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+#pragma unroll
+      for (int k = 4; k < 32; k <<= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], k);
+      const int row = 2 * t + r;
+      if (g == 0) sh.m[warp][row] = m[r], sh.l[warp][row] = l[r];
+      if (row >= rows) continue;
+      float* to = &sh.o[warp][row][g * (D / 8)];
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j)
+        *reinterpret_cast<float4*>(to + 4 * j) = make_float4(o[2 * j][r], o[2 * j][2 + r], o[2 * j + 1][r], o[2 * j + 1][2 + r]);
+    }
+  }
 };
 
 // Whether every piece of a cut unit is there, this CTA's included, which it says first.
@@ -349,17 +568,18 @@ __device__ void empty_rows(const Q8AttendArgs& a, const Q8Sched& sch, int tile_r
   }
 }
 
-template <int D, bool FEW>
-__global__ void __launch_bounds__(kThreads, 1) q8_attend_rows_kernel(const Q8AttendArgs a) {
-  constexpr int kI = FEW ? 1 : 2;  // rows of a lane: g, g + 8
+template <int D, typename Acc>
+__global__ void __launch_bounds__(Acc::kThreads, 1) q8_attend_rows_kernel(const Q8AttendArgs a) {
+  constexpr int kTileRows = Acc::kTileRows, kWarps = Acc::kWarps;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Q8Sched sch;
   __shared__ int s_last;
-  RowsShared<D>& sh = *reinterpret_cast<RowsShared<D>*>(smem);  // over the rings, once they are done with
+  typename Acc::Shared& sh = *reinterpret_cast<typename Acc::Shared*>(smem);  // over the rings, once they are done with
   pdl_wait();
   pdl_trigger();
-  const int nrt = (a.Nq + kRows - 1) / kRows;
-  q8_build_sched(&sch, a.c.len, a.c.cap, a.c.H, nrt, kTile, 1, 1, gridDim.x, kMinTiles, true);
+  const int nrt = (a.Nq + kTileRows - 1) / kTileRows;
+  // a CTA's share is at least one 32-token step for each warp
+  q8_build_sched(&sch, a.c.len, a.c.cap, a.c.H, nrt, kTile, 1, 1, gridDim.x, kWarps * kSub / kTile, true);
   Q8Split S{&sch, a.c.H, nrt, 1, 1};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int blocks = a.c.cap >> a.c.shift;
@@ -372,14 +592,14 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_rows_kernel(const Q8Att
   while (walk.next(S, pc, false)) {
     const int n = q8_len(a.c.len, pc.h, a.c.cap);
     const int end = min(pc.j1 * kTile, n);
-    const int rows = min(kRows, a.Nq - pc.r * kRows);
-    const size_t row0 = static_cast<size_t>(pc.h) * a.Nq + pc.r * kRows;
+    const int rows = min(kTileRows, a.Nq - pc.r * kTileRows);
+    const size_t row0 = static_cast<size_t>(pc.h) * a.Nq + pc.r * kTileRows;
     const uint8_t* K = a.c.K + static_cast<size_t>(pc.h) * a.c.cap * D;
     const uint8_t* V = a.c.V + static_cast<size_t>(pc.h) * a.c.cap * D;
     const float* ks = a.c.ks + static_cast<size_t>(pc.h) * blocks;
     const float* vs = a.c.vs + static_cast<size_t>(pc.h) * blocks;
-    QFrag<D, FEW> q;
-    q.fetch(static_cast<const __nv_bfloat16*>(a.Q) + row0 * D, rows, g, t);
+    Acc acc;
+    acc.q.fetch(static_cast<const __nv_bfloat16*>(a.Q) + row0 * D, rows, g, t);
     constexpr int kHop = kWarps * kSub;
     const int first = pc.j0 * kTile + warp * kSub;
 #pragma unroll
@@ -399,15 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_rows_kernel(const Q8Att
     };
     scales(first);
     if (sch.chunk == 0) q8_unit_pieces(S, pc.h, pc.r, pc);
-    q.widen(a.scale);
-    float o[D / 8][4];  // FEW: rows g + 8 stay 0
-#pragma unroll
-    for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[j][k] = 0.f;
-    float m[kI], l[kI];
-#pragma unroll
-    for (int i = 0; i < kI; ++i) m[i] = -INFINITY, l[i] = 0.f;
+    acc.begin(a.scale, t);
     int stage = 0;
     for (int kb = first; kb < end; kb += kHop) {
       __syncwarp();  // every lane is done with the stage that is fetched into next
@@ -420,114 +632,46 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_rows_kernel(const Q8Att
       __syncwarp();
       KWords<D> kw;
       kw.load(ring + stage * kStage, g, t);
-      float kf[2], lv[2], iv[2];
+      StepScales sc;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        kf[u] = nk[u];
-        lv[u] = log2f(nv[u]);
-        iv[u] = 1.f / nv[u];
+        sc.kf[u] = nk[u];
+        sc.lv[u] = log2f(nv[u]);
+        sc.iv[u] = 1.f / nv[u];
       }
       if (kb + kHop < end) scales(kb + kHop);
-      float s[4][4];
-      kw.template dots<FEW>(q, s);
-      float mt[kI];
-#pragma unroll
-      for (int i = 0; i < kI; ++i) mt[i] = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int k = 0; k < 2 * kI; ++k) {
-          const int key = kb + 8 * j + 2 * t + (k & 1);
-          const float x = fmaf(s[j][k], q.coef[k >> 1] * kf[j >> 1], lv[j >> 1]);
-          s[j][k] = key < end ? x : -INFINITY;
-          mt[k >> 1] = fmaxf(mt[k >> 1], s[j][k]);
-        }
-      bool moved = false;
-#pragma unroll
-      for (int i = 0; i < kI; ++i) {
-        mt[i] = quad_max(mt[i]);
-        moved |= mt[i] > m[i];
-      }
-      if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-        for (int i = 0; i < kI; ++i) {
-          const float mn = fmaxf(m[i], mt[i]);
-          const float al = mn == -INFINITY ? 1.f : exp2f(m[i] - mn);
-          m[i] = mn;
-          l[i] *= al;
-#pragma unroll
-          for (int j = 0; j < D / 8; ++j) {
-            o[j][2 * i] *= al;
-            o[j][2 * i + 1] *= al;
-          }
-        }
-      }
-      VWords<D> vw;
-      vw.load(ring + stage * kStage + 32 * D, g, t);
+      acc.step(kw, ring + stage * kStage + 32 * D, sc, kb, end, g, t);
       stage = stage == kRing - 1 ? 0 : stage + 1;
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        uint32_t p[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-        for (int i = 0; i < kI; ++i) {
-          // a row whose every score is -inf so far (NaN queries aside) keeps P = 0
-          const float b = (m[i] == -INFINITY ? 0.f : -m[i]) + kPBias;
-          float r = 0.f;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float x = ex2_approx(s[2 * u + j][2 * i] + b), y = ex2_approx(s[2 * u + j][2 * i + 1] + b);
-            r += x + y;
-            p[2 * j + i] = pack_f16x2(x, y);
-          }
-          l[i] = fmaf(r, iv[u], l[i]);
-        }
-        vw.accumulate(u, p, o);
-      }
     }
-    // merge the eight warps: maxima first, then every output weighted by its warp
-#pragma unroll
-    for (int i = 0; i < kI; ++i) l[i] = quad_sum(l[i]);
+    // merge the warps: maxima first, then every output weighted by its warp
     cp_async_wait<0>();
     __syncthreads();  // every warp is done with its ring
-    if (t == 0) {
-#pragma unroll
-      for (int i = 0; i < kI; ++i) sh.m[warp][g + 8 * i] = m[i], sh.l[warp][g + 8 * i] = l[i];
-    }
-#pragma unroll
-    for (int k = 0; k < 2 * kI; ++k) {
-      const int row = g + 8 * (k >> 1);
-      if (row >= rows) continue;
-      float* to = &sh.o[warp][row][(2 * t + (k & 1)) * (D / 8)];
-#pragma unroll
-      for (int j = 0; j < D / 8; j += 4)
-        *reinterpret_cast<float4*>(to + j) = make_float4(o[j][k], o[j + 1][k], o[j + 2][k], o[j + 3][k]);
-    }
+    acc.leave(sh, warp, rows, g, t);
     __syncthreads();
     float* slot = a.part + static_cast<size_t>(blockIdx.x * 2 + pc.which) * slot_floats<D>();
-    for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
+    for (int i = threadIdx.x; i < rows * (D / 4); i += Acc::kThreads) {
       const int row = i / (D / 4), c = (i % (D / 4)) * 4;
       float M = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sh.m[w][row]);
       float L = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float f = M == -INFINITY ? 1.f : exp2f(sh.m[w][row] - M);
         const float4 x = *reinterpret_cast<const float4*>(&sh.o[w][row][c]);
         L = fmaf(f, sh.l[w][row], L);
-        acc.x = fmaf(f, x.x, acc.x);
-        acc.y = fmaf(f, x.y, acc.y);
-        acc.z = fmaf(f, x.z, acc.z);
-        acc.w = fmaf(f, x.w, acc.w);
+        sum.x = fmaf(f, x.x, sum.x);
+        sum.y = fmaf(f, x.y, sum.y);
+        sum.z = fmaf(f, x.z, sum.z);
+        sum.w = fmaf(f, x.w, sum.w);
       }
       if (pc.npieces == 1) {
         const float inv = 1.f / L;
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + (row0 + row) * D + c) =
-            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-        if (a.lse && c == 0) a.lse[row0 + row] = (M - kPBias + log2f(L)) * kLn2;
+        put_row4<__nv_bfloat16, D>(a.O, row0 + row, c, make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv));
+        if (a.lse && c == 0) a.lse[row0 + row] = (M - Acc::kBias + log2f(L)) * kLn2;
       } else {
-        *reinterpret_cast<float4*>(slot + row * D + c) = acc;
+        *reinterpret_cast<float4*>(slot + row * D + c) = sum;
         if (c == 0) {
           slot[kRows * D + row] = M;
           slot[kRows * D + kRows + row] = L;
@@ -537,11 +681,11 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_rows_kernel(const Q8Att
     if (pc.npieces > 1) {
       __syncthreads();  // the warps' outputs have been read
       float* s_w = reinterpret_cast<float*>(smem);
-      finish_unit<D, __nv_bfloat16, kRows>(a, pc, row0, rows, kPBias, s_w, s_w + kRows * kQ8MaxCtas, &s_last);
+      finish_unit<D, __nv_bfloat16, kTileRows>(a, pc, row0, rows, Acc::kBias, s_w, s_w + kTileRows * kQ8MaxCtas, &s_last);
     }
     __syncthreads();  // the merge is done with the shared memory
   }
-  empty_rows<D, __nv_bfloat16>(a, sch, kRows, nrt);
+  empty_rows<D, __nv_bfloat16>(a, sch, kTileRows, nrt);
 }
 
 // ------------------------------------------------------------------ f32 rows
@@ -695,18 +839,61 @@ __global__ void __launch_bounds__(kF32Threads) q8_attend_f32_kernel(const Q8Atte
 template <int D, bool FEW>
 struct WeightRows {
   static constexpr int kI = FEW ? 1 : 2;
-  QFrag<D, FEW> q;
-  float z[kI];  // -lse log2 e; -inf: no such row, or one that saw nothing, which weighs nothing
+  QFrag<D, kI> q;
+  // of rows g, g + 8, or 2 t, 2 t + 1 of at most eight.  z: -lse log2 e; -inf: no such row,
+  // or one that saw nothing, which weighs nothing
+  float coef[2], z[2];
   __device__ __forceinline__ void load(const Q8MassArgs& a, int h, int r0, int g, int t) {
     const size_t row0 = static_cast<size_t>(h) * a.Nq + r0;
     const int rows = min(kRows, a.Nq - r0);
     q.fetch(static_cast<const __nv_bfloat16*>(a.Q) + row0 * D, rows, g, t);
 #pragma unroll
-    for (int i = 0; i < kI; ++i) {
-      const float v = g + 8 * i < rows ? a.lse[row0 + g + 8 * i] : -INFINITY;
+    for (int i = 0; i < 2; ++i) {
+      const int row = FEW ? 2 * t + i : g + 8 * i;
+      const float v = row < rows ? a.lse[row0 + row] : -INFINITY;
       z[i] = v == -INFINITY ? -INFINITY : -v * kLog2e;
     }
     q.widen(a.scale);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) coef[i] = FEW ? __shfl_sync(0xffffffffu, q.coef[0], 4 * (2 * t + i)) : q.coef[i % kI];
+  }
+  // the weights of 32 tokens, summed over the rows; token mine(g, t) of them returned
+  static __device__ __forceinline__ int mine(int g, int t) { return FEW ? 8 * t + g : 8 * (g >> 1) + 2 * t + (g & 1); }
+  __device__ __forceinline__ void add(const KWords<D>& kw, const float (&kf)[2], float (&w)[4][2]) const {
+    if constexpr (FEW) {
+      float s[2][4];
+      kw.dots_few(q, s);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[2 * u + (k >> 1)][0] += ex2_approx(fmaf(s[u][k], coef[k & 1] * kf[u], z[k & 1]));
+    } else {
+      float s[4][4];
+      kw.dots(q, s);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[j][k & 1] += ex2_approx(fmaf(s[j][k], coef[k >> 1] * kf[j >> 1], z[k >> 1]));
+    }
+  }
+  static __device__ __forceinline__ float total(const float (&w)[4][2], int g, int t) {
+    float v = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (FEW) {
+        const float x = quad_sum(w[j][0]);  // token 8 j + g
+        if (t == j) v = x;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float x = w[j][i];
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+          if (g == 2 * j + i) v = x;
+        }
+      }
+    }
+    return v;
   }
 };
 
@@ -727,8 +914,8 @@ __global__ void __launch_bounds__(kThreads, FEW ? 2 : 1) q8_mass_rows_kernel(con
   next.load_global(K, kb, n - 1, g, t);
   WeightRows<D, FEW> rows;
   if constexpr (ONE) rows.load(a, h, 0, g, t);
-  // lane (g, t) stores tokens 8 j + 2 t + i where g = 2 j + i, and fetches what it adds to
-  const int mine = 8 * (g >> 1) + 2 * t + (g & 1);
+  // the token whose weight this lane stores, and fetches what it adds to
+  const int mine = WeightRows<D, FEW>::mine(g, t);
   for (; kb < n; kb += hop) {
     const KWords<D> kw = next;
     float kf[2], w[4][2], before = 0.f;
@@ -740,24 +927,9 @@ __global__ void __launch_bounds__(kThreads, FEW ? 2 : 1) q8_mass_rows_kernel(con
     for (int j = 0; j < 4; ++j) w[j][0] = w[j][1] = 0.f;
     for (int r0 = 0; r0 < (ONE ? 1 : a.Nq); r0 += kRows) {
       if constexpr (!ONE) rows.load(a, h, r0, g, t);
-      float s[4][4];
-      kw.template dots<FEW>(rows.q, s);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int k = 0; k < 2 * WeightRows<D, FEW>::kI; ++k)
-          w[j][k & 1] += ex2_approx(fmaf(s[j][k], rows.q.coef[k >> 1] * kf[j >> 1], rows.z[k >> 1]));
+      rows.add(kw, kf, w);
     }
-    float v = 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float x = w[j][i];
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (g == 2 * j + i) v = x;
-      }
+    const float v = WeightRows<D, FEW>::total(w, g, t);
     if (kb + mine < n) a.mass[m0 + kb + mine] = a.prev ? fmaf(a.decay, before, v) : v;
   }
 }
@@ -820,17 +992,17 @@ __global__ void __launch_bounds__(kThreads, 2) q8_mass_f32_kernel(const Q8MassAr
 
 int split_grid(int n_sm) { return n_sm < kQ8MaxCtas ? n_sm : kQ8MaxCtas; }
 
-template <int D, bool FEW>
+template <int D, typename Acc>
 cudaError_t attend_rows(const Q8AttendArgs& a, int n_sm, cudaStream_t st) {
   const int grid = split_grid(n_sm);
-  constexpr size_t ring = kWarps * kRing * 64 * D, shared = sizeof(RowsShared<D>);
+  constexpr size_t ring = Acc::kWarps * kRing * 64 * D, shared = sizeof(typename Acc::Shared);
   constexpr size_t smem = ring > shared ? ring : shared;
-  static_assert(smem >= 2 * kRows * kQ8MaxCtas * sizeof(float), "the merge's weights fit");
-  const cudaError_t e = cudaFuncSetAttribute(q8_attend_rows_kernel<D, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
+  static_assert(smem >= 2 * Acc::kTileRows * kQ8MaxCtas * sizeof(float), "the merge's weights fit");
+  const auto kernel = q8_attend_rows_kernel<D, Acc>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   LaunchTrace trace("q8_attend_rows_kernel", st);
-  return launch_pdl(q8_attend_rows_kernel<D, FEW>, dim3(grid), dim3(kThreads), smem, st, a);
+  return launch_pdl(kernel, dim3(grid), dim3(Acc::kThreads), smem, st, a);
 }
 
 template <int D>
@@ -851,8 +1023,8 @@ int mass_blocks(int cap, int per_cta, int H, int n_sm, int waves) {
 }  // namespace
 
 cudaError_t launch_q8_attend_rows(const Q8AttendArgs& a, int n_sm, cudaStream_t st) {
-  if (a.Nq <= 8) return a.c.d == 128 ? attend_rows<128, true>(a, n_sm, st) : attend_rows<64, true>(a, n_sm, st);
-  return a.c.d == 128 ? attend_rows<128, false>(a, n_sm, st) : attend_rows<64, false>(a, n_sm, st);
+  if (a.Nq <= 8) return a.c.d == 128 ? attend_rows<128, FewAcc<128>>(a, n_sm, st) : attend_rows<64, FewAcc<64>>(a, n_sm, st);
+  return a.c.d == 128 ? attend_rows<128, RowsAcc<128>>(a, n_sm, st) : attend_rows<64, RowsAcc<64>>(a, n_sm, st);
 }
 cudaError_t launch_q8_attend_f32(const Q8AttendArgs& a, int n_sm, cudaStream_t st) {
   return a.c.d == 128 ? attend_f32<128>(a, n_sm, st) : attend_f32<64>(a, n_sm, st);
