@@ -480,9 +480,10 @@ __device__ __forceinline__ void put_row4(void* O, size_t row, int c, float4 v) {
 }
 
 // A piece that finds all pieces of its unit there merges them, in their order: their maxima
-// and sums, fetched at once, become one weight per (row, piece); then the outputs, with
-// eight fetches in flight.  (A second kernel for it cost 6 us.)  Called by the whole CTA
-// after it has stored its own piece; s_w, s_l: shared memory, ROWS x kQ8MaxCtas each.
+// and sums, fetched at once, become one weight per (row, piece), and weigh the outputs,
+// sixteen of which are on their way meanwhile.  (A second kernel for it cost 6 us.)  Called
+// by the whole CTA after it has stored its own piece; s_w, s_l: shared memory, ROWS x
+// kQ8MaxCtas each.
 template <int D, typename T, int ROWS>
 __device__ void finish_unit(const Q8AttendArgs& a, const Q8Piece& pc, size_t row0, int rows, float bias, float* s_w,
                             float* s_l, int* s_last) {
@@ -499,6 +500,15 @@ __device__ void finish_unit(const Q8AttendArgs& a, const Q8Piece& pc, size_t row
   const float* first = a.part + static_cast<size_t>(pc.cfirst * 2 + pc.wfirst) * slot_floats<D>();
   const float* rest = a.part + static_cast<size_t>(pc.cfirst) * 2 * slot_floats<D>();  // piece k > 0: slot 0 of CTA cfirst + k
   auto slot = [&](int k) { return k == 0 ? first : rest + static_cast<size_t>(k) * 2 * slot_floats<D>(); };
+  // a thread's first outputs of the first sixteen pieces, in flight with the maxima and sums
+  constexpr int kAhead = 16;
+  float4 x[kAhead];
+  auto outputs = [&](int row, int c, int k0) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (k0 + u < np) x[u] = __ldcg(reinterpret_cast<const float4*>(slot(k0 + u) + row * D + c));
+  };
+  if (tid < rows * (D / 4)) outputs(tid / (D / 4), (tid % (D / 4)) * 4, 0);
   for (int i = tid; i < rows * np; i += nthreads) {
     const int row = i / np, k = i - row * np;
     s_w[row * kQ8MaxCtas + k] = __ldcg(slot(k) + kRows * D + row);
@@ -531,13 +541,10 @@ __device__ void finish_unit(const Q8AttendArgs& a, const Q8Piece& pc, size_t row
     const int row = i / (D / 4), c = (i % (D / 4)) * 4;
     const float* w = s_w + row * kQ8MaxCtas;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < np; k0 += 8) {
-      float4 x[8];
+    for (int k0 = 0; k0 < np; k0 += kAhead) {
+      if (i != tid || k0 != 0) outputs(row, c, k0);
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
-        if (k0 + u < np) x[u] = __ldcg(reinterpret_cast<const float4*>(slot(k0 + u) + row * D + c));
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < kAhead; ++u) {
         if (k0 + u >= np) continue;
         const float f = w[k0 + u];
         acc.x = fmaf(f, x[u].x, acc.x);
