@@ -45,7 +45,9 @@ struct Scratch {
   size_t bytes = 0;
 };
 
-bool chunk_kernel(int32_t rows, kvb_dtype dtype) { return dtype == KVB_BF16 && rows >= kQ8ChunkRows; }
+bool chunk_kernel(const kvb_q8_cache* c, int32_t rows, kvb_dtype dtype) {
+  return dtype == KVB_BF16 && rows >= q8_chunk_rows(c->heads, c->capacity);
+}
 
 Scratch scratch(const kvb_q8_cache* c, int32_t max_queries, kvb_dtype dtype, void* ws) {
   Scratch s;
@@ -55,7 +57,7 @@ Scratch scratch(const kvb_q8_cache* c, int32_t max_queries, kvb_dtype dtype, voi
   s.part = a.take<float>(q8_part_floats(c->head_dim));
   s.kept = e.take<int>(static_cast<size_t>(c->heads) * c->capacity);
   s.bytes = a.bytes() > e.bytes() ? a.bytes() : e.bytes();
-  if (chunk_kernel(max_queries, dtype)) {
+  if (chunk_kernel(c, max_queries, dtype)) {
     const size_t rows = static_cast<size_t>(c->heads) * max_queries;
     s.chunk.hi = q.take<uint8_t>(rows * c->head_dim);
     s.chunk.lo = q.take<uint8_t>(rows * c->head_dim);
@@ -157,7 +159,7 @@ kvb_status kvb_q8_attend(const kvb_q8_cache* c, const void* Q, int32_t Nq, kvb_d
   a.tag = next_tag();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == KVB_F32) return cuda_status(launch_q8_attend_f32(a, dev.n_sm, st));
-  if (chunk_kernel(Nq, dtype)) return cuda_status(launch_q8_attend_chunk(a, s.chunk, dev.n_sm, st));
+  if (chunk_kernel(c, Nq, dtype)) return cuda_status(launch_q8_attend_chunk(a, s.chunk, dev.n_sm, st));
   return cuda_status(launch_q8_attend_rows(a, dev.n_sm, st));
 }
 
@@ -182,7 +184,7 @@ kvb_status kvb_q8_mass(const kvb_q8_cache* c, const void* Q, int32_t Nq, kvb_dty
   a.mass = c->mass;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == KVB_F32) return cuda_status(launch_q8_mass_f32(a, dev.n_sm, st));
-  if (chunk_kernel(Nq, dtype)) return cuda_status(launch_q8_mass_chunk(a, s.chunk, dev.n_sm, st));
+  if (chunk_kernel(c, Nq, dtype)) return cuda_status(launch_q8_mass_chunk(a, s.chunk, dev.n_sm, st));
   return cuda_status(launch_q8_mass_rows(a, dev.n_sm, st));
 }
 

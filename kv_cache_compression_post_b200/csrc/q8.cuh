@@ -328,17 +328,19 @@ constexpr int kQ8MassCounters = kQ8MaxCtas * 2 * 8;  // arrival counters of the 
 cudaError_t launch_q8_attend_chunk(const Q8AttendArgs& a, const Q8ChunkScratch& s, int n_sm, cudaStream_t st);
 
 // Rows per head from which a bf16 call takes the tcgen05 kernel (128 or 256 rows at once,
-// however few there are) instead of 16-row tiles, each of which reads the cache again.
+// however few there are) instead of 16-row tiles, each of which reads the cache again:
+// more where the cache is so small that beginnings and merges are what takes time.
 // us measured, 16-row tiles / tcgen05, head_dim 128:
-//   attention   heads x tokens   32 rows     48 rows     64 rows     128 rows
-//               12 x 15600       37 / 62     47 / 62     57 / 62     104 / 64
-//               8 x 131072       129 / 160   183 / 160   265 / 162   509 / 160
-//               1 x 8192         18 / 37     18 / 37     19 / 37     19 / 38
-//               64 x 1024        32 / 46     40 / 46     45 / 46     71 / 49
-//   weights     12 x 15600       21 / 27     27 / 27     33 / 27     57 / 27
-//               8 x 131072       84 / 111    110 / 112   137 / 112   242 / 112
-//               64 x 1024        9 / 16      11 / 16     14 / 16     22 / 16
-constexpr int kQ8ChunkRows = 49;
+//   attention   heads x tokens   32 rows     48 rows     64 rows     96 rows     128 rows
+//               12 x 15600       33 / 61     42 / 62     50 / 63     66 / 64     89 / 64
+//               8 x 131072       107 / 150   150 / 150   214 / 151   278 / 152   406 / 152
+//               1 x 8192         15 / 38     16 / 38     16 / 38     17 / 39     16 / 39
+//               64 x 1024        30 / 46     37 / 46     42 / 46     53 / 47     64 / 47
+//   weights     12 x 15600       20 / 28     26 / 29     32 / 29     44 / 29     55 / 29
+//               8 x 131072       74 / 113    101 / 114   127 / 114   180 / 114   234 / 114
+//               1 x 8192         7 / 11      7 / 11      7 / 11      9 / 11      11 / 11
+//               64 x 1024        9 / 18      11 / 18     13 / 18     17 / 18     22 / 18
+inline int q8_chunk_rows(long long heads, long long capacity) { return heads * capacity <= 131072 ? 81 : 49; }
 
 struct Q8EvictArgs {
   Q8View src;

@@ -222,6 +222,25 @@ def test_attend_split_work(heads, lens, rows):
     check_attend(c, Q, O, lse, rows=None if heads < 40 else np.array([0, rows // 2, rows - 1]))
 
 
+@pytest.mark.parametrize("rows", [48, 49, 63, 80, 81])
+@pytest.mark.parametrize("heads,cap", [(2, 65536), (3, 65536)])
+def test_rows_between_the_kernels(heads, cap, rows):
+    """Row counts on either side of the choice of kernel, for a small and a larger cache, with a
+    workspace of exactly their size."""
+    import torch
+    c = filled(heads, 64, cap, 128, "bf16", [900, 0, 130][:heads], rows, max_queries=rows)
+    Q = torch.randn(heads, rows, 64, device="cuda").bfloat16()
+    c.mass.zero_()
+    O, lse = attend(c, Q)
+    c.accumulate(Q, lse)
+    assert c.status() == 0
+    check_attend(c, Q, O, lse)
+    for h in range(heads):                  # every row's weights sum to 1
+        n = int(c.len[h])
+        assert abs(float(c.mass[h, :n].double().sum()) - (rows if n else 0)) <= rows * 2.0 ** -10
+        assert bool((c.mass[h, n:] == 0).all())
+
+
 @pytest.mark.parametrize("dtype,rows", [("bf16", 3), ("bf16", 140), ("f32", 3)])
 def test_attend_sharp_and_scaled(dtype, rows):
     """Scores far apart (one token takes all), a late maximum, uneven scales of V by 2^40,
@@ -260,7 +279,7 @@ def test_attend_non_finite_queries_stay_in_their_row(rows, dtype):
     assert torch.equal(O[keep], clean[keep]) and torch.equal(lse[keep], clean_lse[keep])
 
 
-@pytest.mark.parametrize("dtype,rows", [("bf16", 1), ("bf16", 20), ("bf16", 70), ("f32", 3)])
+@pytest.mark.parametrize("dtype,rows", [("bf16", 1), ("bf16", 20), ("bf16", 70), ("bf16", 100), ("f32", 3)])
 def test_attend_scores_past_the_range_of_floats(rows, dtype):
     """The first 300 tokens' scores lie below -2^128 and count as -inf: they weigh nothing,
     and nothing else is touched."""
