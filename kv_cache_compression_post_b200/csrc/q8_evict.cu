@@ -2,8 +2,9 @@
 //
 // q8_select_kernel, a cluster of eight CTAs per head: the weight of the last token to
 // stay is found digit by digit (8 bits of the order-preserving integer of a float, from
-// the top: a radix select, four passes over keys held in shared memory, the CTAs'
-// histograms added over distributed shared memory), then each warp counts and writes the
+// the top: a radix select, up to four passes over keys held in shared memory, the CTAs'
+// histograms exchanged over distributed shared memory; over once all keys of the digits
+// found stay), then each warp counts and writes the
 // positions of its own run of tokens, so the list comes out in order and of equal weights
 // the lower positions stay.  Bound by latency: a head has one answer per pass to wait for
 // (one CTA per head took 150 us for 8 heads of 131072 tokens).
@@ -33,24 +34,27 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 
 struct SelShared {
   uint32_t key[kSelKeys];
+  alignas(16) int in[2][kSelCtas][256];  // by parity of the pass: every CTA's digit counts, largest digit first
   int hist[kCopies][257];  // a bin's copies in different banks
-  int sum[2][256];     // this CTA's digit counts, by parity of the pass
-  int total[256];      // the head's
   int above[kSelWarps], equal[kSelWarps];
-  int cta[2];          // this CTA's
+  int cta[2][kSelCtas];  // every CTA's
   uint32_t prefix;
   int need;
+  bool done;
 };
 
 __global__ void __cluster_dims__(kSelCtas, 1, 1) __launch_bounds__(kSelThreads) q8_select_kernel(const Q8EvictArgs a) {
-  extern __shared__ uint8_t smem[];
+  extern __shared__ __align__(16) uint8_t smem[];
   SelShared& s = *reinterpret_cast<SelShared*>(smem);
   cg::cluster_group cluster = cg::this_cluster();
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   pdl_wait();
   pdl_trigger();
   const int rank = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n = q8_len(a.src.len, h, a.src.cap);
   int* kept = a.kept + static_cast<size_t>(h) * a.budget;
+  // every CTA of the cluster runs: its shared memory may be written to
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   if (n <= a.budget) {
     for (int i = rank * kSelThreads + tid; i < n; i += kSelCtas * kSelThreads) kept[i] = i;
     if (rank == 0 && tid == 0) a.len[h] = n;
@@ -75,12 +79,13 @@ __global__ void __cluster_dims__(kSelCtas, 1, 1) __launch_bounds__(kSelThreads) 
     if (tid == 0) {
       s.prefix = 0u;
       s.need = need;
+      s.done = false;
     }
+    for (int i = tid; i < kCopies * 257; i += kSelThreads) (&s.hist[0][0])[i] = 0;
+    __syncthreads();
     const int p0 = max(c0, lo), p1 = min(c1, hi);
     for (int pass = 0; pass < 4; ++pass) {
       const int shift = 24 - 8 * pass;
-      for (int i = tid; i < kCopies * 257; i += kSelThreads) (&s.hist[0][0])[i] = 0;
-      __syncthreads();
       const uint32_t prefix = s.prefix;
       const int want = s.need;
       const uint32_t mask = pass == 0 ? 0u : 0xFFFFFFFFu << (shift + 8);
@@ -89,25 +94,27 @@ __global__ void __cluster_dims__(kSelCtas, 1, 1) __launch_bounds__(kSelThreads) 
         if ((k & mask) == prefix) atomicAdd(&s.hist[tid % kCopies][(k >> shift) & 255u], 1);
       }
       __syncthreads();
+      // every CTA gives its counts to all, so that after the barrier they are read locally
       if (tid < 256) {
         int v = 0;
 #pragma unroll
         for (int c = 0; c < kCopies; ++c) v += s.hist[c][tid];
-        s.sum[pass & 1][tid] = v;
+#pragma unroll
+        for (int c = 0; c < kSelCtas; ++c) cluster.map_shared_rank(&s.in[pass & 1][rank][0], c)[255 - tid] = v;
       }
       cluster.sync();
-      if (tid < 256) {
-        int v = 0;
-#pragma unroll
-        for (int c = 0; c < kSelCtas; ++c) v += cluster.map_shared_rank(&s.sum[pass & 1][0], c)[tid];
-        s.total[tid] = v;
-      }
-      __syncthreads();
       if (warp == 0) {
         // keys of larger digits, eight digits a lane, from the top
-        int v[8], mine = 0;
+        int v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, mine = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) mine += v[k] = s.total[255 - lane * 8 - k];
+        for (int c = 0; c < kSelCtas; ++c) {
+          const int4* x = reinterpret_cast<const int4*>(&s.in[pass & 1][c][lane * 8]);
+          const int4 a4 = x[0], b4 = x[1];
+          v[0] += a4.x, v[1] += a4.y, v[2] += a4.z, v[3] += a4.w;
+          v[4] += b4.x, v[5] += b4.y, v[6] += b4.z, v[7] += b4.w;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mine += v[k];
         int above = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -119,13 +126,24 @@ __global__ void __cluster_dims__(kSelCtas, 1, 1) __launch_bounds__(kSelThreads) 
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             if (above < want && above + v[k] >= want) {
-              s.prefix = prefix | (static_cast<uint32_t>(255 - lane * 8 - k) << shift);
+              const uint32_t to = prefix | (static_cast<uint32_t>(255 - lane * 8 - k) << shift);
+              s.prefix = to;
               s.need = want - above;
+              // all keys with these digits stay: those above the largest key without them
+              if (above + v[k] == want && to > 0) {
+                s.done = true;
+                s.prefix = to - 1;
+                s.need = 0;
+              }
             }
             above += v[k];
           }
         }
       }
+      __syncthreads();
+      if (s.done) break;
+      // (between the barrier and the scan above, these stores cost 3 us in all)
+      for (int i = tid; i < kCopies * 257; i += kSelThreads) (&s.hist[0][0])[i] = 0;
       __syncthreads();
     }
     thr = s.prefix;
@@ -153,23 +171,16 @@ __global__ void __cluster_dims__(kSelCtas, 1, 1) __launch_bounds__(kSelThreads) 
     s.equal[warp] = equal_n;
   }
   __syncthreads();
-  if (tid < 2) {
-    const int* v = tid ? s.equal : s.above;
-    int x = 0;
-    for (int w = 0; w < kSelWarps; ++w) x += v[w];
-    s.cta[tid] = x;
+  if (warp < 2) {
+    const int x = __reduce_add_sync(0xffffffffu, (warp ? s.equal : s.above)[lane]);
+    if (lane < kSelCtas) *cluster.map_shared_rank(&s.cta[warp][rank], lane) = x;
   }
+  // after which no CTA writes to another, so that each may leave when it is done
   cluster.sync();
-  int at = 0, eq_before = 0;
-  for (int c = 0; c < rank; ++c) {
-    const int* v = cluster.map_shared_rank(&s.cta[0], c);
-    at += v[0];
-    eq_before += v[1];
-  }
-  for (int w = 0; w < warp; ++w) {
-    at += s.above[w];
-    eq_before += s.equal[w];
-  }
+  // what lies before this warp's run: in the CTAs before, in the warps before
+  const int at_cta = lane < rank ? s.cta[0][lane] : 0, eq_cta = lane < rank ? s.cta[1][lane] : 0;
+  int at = __reduce_add_sync(0xffffffffu, at_cta + (lane < warp ? s.above[lane] : 0));
+  int eq_before = __reduce_add_sync(0xffffffffu, eq_cta + (lane < warp ? s.equal[lane] : 0));
   at += min(eq_before, quota);
   const uint32_t below = (1u << lane) - 1u;
   for (int i = r0; i < r1; i += 32) {
@@ -183,7 +194,6 @@ __global__ void __cluster_dims__(kSelCtas, 1, 1) __launch_bounds__(kSelThreads) 
     eq_before += __popc(em);
   }
   if (rank == 0 && tid == 0) a.len[h] = a.budget;
-  cluster.sync();  // no CTA leaves while another reads its counts
 }
 
 constexpr int kGatherThreads = 256;

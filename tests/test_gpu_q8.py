@@ -694,6 +694,27 @@ def test_workspace_needs_no_initialisation(rows):
     check_attend(c, Q, O, lse, rows=np.array([0, rows - 1]))
 
 
+@pytest.mark.parametrize("low", [1e-30, 0.999, -1.0, float("nan")])
+@pytest.mark.parametrize("more", [-1, 0, 1])
+def test_evict_where_a_digit_decides(low, more):
+    """Two weights, and a budget of as many as have the larger, one less and one more: all keys
+    of a digit stay, at the first or a later digit, or all but one."""
+    import torch
+    import kv_cache_compression_post_b200 as kvb
+    n, sink, recent = 5000, 3, 5
+    c = filled(2, 64, 5008, 16, "bf16", [n, n - 1], 1)
+    mass = torch.full((n,), low, device="cuda")
+    mass[sink + 1:n - recent - 1:3] = 1.0
+    c.mass[:, :n] = mass
+    budget = int((mass == 1.0).sum()) + sink + recent + more
+    to = kvb.Q8Cache(2, 64, -(-budget // 16) * 16, 16)
+    kept = torch.empty(2, budget, dtype=torch.int32, device="cuda")
+    c.evict(to, budget, sink=sink, recent=recent, kept=kept)
+    for h, m in enumerate((n, n - 1)):
+        want = q8.keep(c.mass[h].double().cpu().numpy(), m, budget, sink, recent)
+        np.testing.assert_array_equal(kept[h].cpu().numpy(), want)
+
+
 def test_evict_more_tokens_than_shared_memory_holds():
     """200001 tokens of one head (a cluster keeps the keys of 131072 between its passes), and
     a budget of none but ties."""
