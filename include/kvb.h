@@ -436,12 +436,17 @@ KVB_API kvb_status kvb_rope(const void* X, const int32_t* pos, int32_t heads, in
  * callers that manage their own caches: rows are appended, attended, weighed and
  * cut to a budget in place of the bank's density or similarity policy.
  *
+ * Every call runs on the current device, where all of its arrays have to lie.
+ *
  * A cached value is code * scale: code in FP8 E4M3 (the encoding of
  * KVB_STORE_FP8_E4M3), scale the f32 of its (head, block of `block` tokens), K and
  * V apart.  kvb_q8_append writes power-of-two scales, the smallest with
  * max|x| / scale <= 448 over the block, so scaling loses nothing and the only
  * rounding is E4M3's (step 2^-3 of a value's binade, above 2^-15 of the block's
- * largest).  The attention and weight kernels accept any positive finite scale.
+ * largest); a block of zeros has 2^-100.  The attention and weight kernels accept any
+ * positive finite scale; the V scales of a head have to lie within 2^100 of one another
+ * (bf16 attention leaves out tokens whose weight times V scale is below about 2^-130
+ * of the largest).
  *
  * Sequences of a batch are further heads (heads = batch x K/V heads).  Query heads
  * that share a K/V head are further rows of it: [batch][Hq][n][d] queries are, as
@@ -498,8 +503,10 @@ KVB_API kvb_status kvb_q8_append(const kvb_q8_cache* c, const void* K, int64_t k
  * log of the sum of exp(scale q.k)) or NULL; scale > 0, or 0 => 1/sqrt(d).  One query
  * (a single token) up to whole chunks.  bf16 runs on the tensor cores: Q enters as
  * two E4M3 parts of each element or as fp16 with a power of two per row, weights as
- * fp16, sums fp32; f32 runs on CUDA cores (small problems).  Infinite or NaN queries
- * give NaN rows. */
+ * fp16, sums fp32 (elements below 2^-14 of their row's largest, or below 2^-114, lose
+ * bits); f32 runs on CUDA cores (small problems).  Scores below fp32's range count as
+ * -inf; infinite or NaN queries give NaN rows.  O and lse overlap nothing else of the
+ * call. */
 KVB_API kvb_status kvb_q8_attend(const kvb_q8_cache* c, const void* Q, int32_t Nq, kvb_dtype dtype, float scale,
                                  void* O, float* lse, void* workspace, size_t workspace_bytes, void* stream);
 

@@ -23,16 +23,20 @@
 // TMEM: S_A, S_B, O_A, O_B (128 columns each), P_t over S_t's first half.  Per key tile
 // and query tile: S_t, softmax, P_t V, and S_t of the next tile behind it.
 // What bounds it.  A 256 x 128 step has 2048 clk of tensor time and 2048 clk of
-// exponentials per SM and takes ~4400 (at 1.8 GHz, the power cap active): softmax and
+// exponentials per SM and takes ~4100 (at 1.8 GHz, the power cap active): softmax and
 // products of one query tile follow one another, so the two tiles have to alternate.
 // Kept for that, each measured on 12 heads x 4680 queries x 15600 tokens: one MMA warp
 // per query tile, operands in uniform registers (627 -> 557 us with the scales' ring;
-// issuing from one divergent lane cost ~110 clk an MMA), and turns at the exponentials
-// (552 -> 507 us; left alone the tiles fall into step and wait together).  Not kept: a
+// issuing from one divergent lane cost ~110 clk an MMA), turns at the exponentials
+// (552 -> 507 us; left alone the tiles fall into step and wait together), codes widened
+// four at a time (502 -> 481 us).  Not kept: a
 // part of the exponentials as polynomials on the FMA pipe (+6 % for one pair in eight:
 // issue, not the exponential unit, is short in a turn); 64-token steps with two score
 // buffers (542 us: N = 64 products read the query rows twice as often); two warpgroups
-// per query tile, by steps (554 us) or by columns (584 us).
+// per query tile, by steps (554 us) or by columns (584 us); the scores' scaling before
+// the turn (+2 %), or nothing but exponentials in it (+6 %); handing the turn on before
+// its last quarter or half (no gain); P V of the first tokens before the others' P is
+// there (+4 %: the store has to be waited for twice).
 // Warps: 0 loads, 1 and 3 MMAs of tile A and B, 2 TMEM and scales, 4-7 V widening,
 // 8-11 softmax of tile A, 12-15 of tile B (one thread per row).
 #include "host_util.h"

@@ -4,24 +4,25 @@
 // Reading the cache once is the bound (2 bytes per token and channel), so the work is
 // split over its tokens (Q8Split) and every warp streams 32 tokens at a time through a
 // ring of its own in shared memory (cp.async, no barrier between warps) into the
-// fragments of mma.sync.m16n8k16 (16 rows x 8 tokens).  What the layout relies on: a
+// fragments of mma.sync.m16n8k16: 16 rows x 8 tokens, or with at most eight rows
+// 16 tokens (or channels) x 8 rows, half the instructions.  What the layout relies on: a
 // contraction may run over the channels, and over the tokens, in any order that both
 // operands share.  Lane (g, t) = (lane / 4, lane % 4) takes 16 contiguous bytes of token
 // g's K row and uses them as four MMA steps, so Q is fetched in that order of channels;
 // it takes 16 contiguous bytes of V for the four tokens its P columns stand for, and
-// output column n of MMA j is channel 16 n + j.  Codes widen to fp16 exactly, two per
-// instruction, and Q enters as fp16 times a power of two per row (bf16 has 8 bits,
-// fp16 11, so nothing is lost above 2^-14 of the row's largest).
-// What bounds it: widening a pair of codes takes 8 clk of a scheduler's ALU, ~1000 of the
-// ~1500 clk of a 32-token step, beside which the memory would need ~1400 (8 heads, 8 rows,
-// 102400 tokens on average: 41 us of memory alone, 40 us of arithmetic alone, 50 us
-// together, and the merge).  E4M3 operands of mma.sync do not help, they are widened in
-// the same way (same time, measured).
+// row or column n of MMA j is channel 16 n + j.  Codes widen to fp16 exactly, four per
+// word in two instructions, and Q enters as fp16 times a power of two per row (bf16 has
+// 8 bits, fp16 11, so nothing is lost above 2^-14 of the row's largest).
+// What bounds it (at most eight rows): memory.  8 rows over 8 heads, 819200 tokens in all,
+// take 50 us, 49 with the arithmetic taken out; a long cache streams at 5.4 TB/s, and a
+// call takes ~10 us besides (lengths, split and query 5.6, a merge of pieces 4), half
+// of the 19 us of one row over 12 heads of 15600 tokens.  E4M3 operands of mma.sync do
+// not help, they are widened all the same.
 //
 // Softmax in the log2 domain.  With ks, vs the scales of a token's block,
-//     x = (q.k) ks scale log2 e,   P = 2^(x + log2 vs - m + kPBias),
+//     x = (q.k) ks scale log2 e,   P = 2^(x + log2 vs - m + kBias),
 // m the running maximum of x + log2 vs: V's scale rides in the exponent at no cost,
-// P never exceeds 2^kPBias in fp16, and the row sum adds P / vs per block.  Sums,
+// P stays within fp16's range, and the row sum adds P / vs per block.  Sums,
 // maxima and partial outputs are fp32.
 #include "host_util.h"
 #include "q8.cuh"
@@ -34,9 +35,10 @@ namespace {
 
 constexpr int kThreads = 256;  // of the weights' kernels
 constexpr int kWarps = kThreads / 32;
-constexpr int kRowsThreads = 256;      // ten or twelve warps, with their registers cut to fit, were slower
-constexpr int kFewThreads = 256;
-constexpr int kRing = 2;               // stages of a warp's ring (three: 5 % slower)
+// of the attention's; ten or twelve warps, with their registers cut to fit, were slower
+// (at most eight rows x 131072: 51 us with 256 threads, 53 with 320, 52 with 384, 54 with 192)
+constexpr int kRowsThreads = 256, kFewThreads = 256;
+constexpr int kRing = 2;  // stages of a warp's ring (three: 1 to 2 % slower)
 constexpr int kTile = 64;    // tokens per key tile of the split
 constexpr int kSub = 32;     // tokens a warp takes at a time
 constexpr int kRows = 16;    // rows per row tile
