@@ -352,7 +352,7 @@ def test_attend_offsets_past_32_bits(rows):
     Q = torch.randn(H, rows, d, device="cuda").bfloat16()
     O, lse = attend(c, Q)
     assert bool((O[:H - 1] == 0).all())
-    small = filled(1, d, 3072, 128, "bf16", [0], 0, max_queries=rows)
+    small = filled(1, d, 3200, 128, "bf16", [0], 0, max_queries=rows)
     for a, b in ((small.K, c.K), (small.V, c.V), (small.k_scale, c.k_scale), (small.v_scale, c.v_scale)):
         a[0] = b[H - 1, :a.shape[1]]
     small.len[0] = n
