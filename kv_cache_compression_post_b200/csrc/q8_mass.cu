@@ -12,9 +12,10 @@
 // ping-pong between the tensor core and eight epilogue warps each.  A block cut between
 // CTAs is summed, in order, by whichever warp comes last to its 32 keys.
 // What bounds it: exponentials.  A step is 65536 of them, 4096 clk at the unit's 16 per
-// clock and SM, against 2048 clk of tensor time; kPoly of 8 pairs therefore run as
-// polynomials on the FMA pipe (12 heads x 4680 queries x 15600 tokens: 304 us, 309 without
-// and no less with more; 16-row tiles on mma.sync took 2466).
+// clock and SM, against 2048 clk of tensor time (12 heads x 4680 queries x 15600 tokens:
+// 313 us; 16-row tiles on mma.sync took 2466).  One pair in eight as a polynomial on the FMA
+// pipe took 307 us, but its 2^n, put together from bits, is no infinity past 2^128, where a
+// caller's lse far below the scores leads.
 // Warps: 0 loads, 1 MMA, 2 TMEM, 3 column coefficients, 4-11 epilogue of row tile 0,
 // 12-19 of row tile 1 (4 lane quarters x 2 column halves).
 #include "host_util.h"
@@ -30,7 +31,6 @@ constexpr int kThreads = 640;
 constexpr int kRowTile = 128, kBlock = 256, kCols = 256;
 constexpr int kStages = 2;
 constexpr int kBarBytes = 256;
-constexpr int kPoly = 1;  // pairs of 8 whose exponentials run on the FMA pipe
 
 struct alignas(8) Bars {
   uint64_t a_full, a_empty;
@@ -61,33 +61,6 @@ struct Blocks {
   long long total;         // steps
   int G, CT;
 };
-
-__device__ __forceinline__ float fmax_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
-// 2^x of two scores, by the exponential unit or (poly) on the FMA pipe: x = n + f with
-// |f| <= 1/2 (n by the rounding of a large float's last bit), 2^f by the polynomial of
-// degree 4 of least largest relative error on [-1/2, 1/2] (Remez exchange: 2.6e-6, 4e-8 on
-// average), times 2^n put together from n's bits.  There, x is at least -127, whose bits
-// make 2^n a zero; NaN stays NaN.
-__device__ __forceinline__ float2 exp2_pair(float2 x, bool poly) {
-  if (!poly) return make_float2(ex2_approx(x.x), ex2_approx(x.y));
-  constexpr float kBig = 12582912.f;  // 1.5 * 2^23
-  x = make_float2(fmax_nan(x.x, -127.f), fmax_nan(x.y, -127.f));
-  const float2 t = __fadd2_rn(x, make_float2(kBig, kBig));
-  const float2 n = __fadd2_rn(t, make_float2(-kBig, -kBig));
-  const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), x);
-  float2 p = make_float2(0.009570102207362652f, 0.009570102207362652f);
-  p = __ffma2_rn(p, f, make_float2(0.05591785907745361f, 0.05591785907745361f));
-  p = __ffma2_rn(p, f, make_float2(0.240247443318367f, 0.240247443318367f));
-  p = __ffma2_rn(p, f, make_float2(0.6931217908859253f, 0.6931217908859253f));
-  p = __ffma2_rn(p, f, make_float2(0.9999992847442627f, 0.9999992847442627f));
-  return __fmul2_rn(p, make_float2(__int_as_float((__float_as_int(t.x) << 23) + 0x3F800000),
-                                   __int_as_float((__float_as_int(t.y) << 23) + 0x3F800000)));
-}
 
 // One CTA's steps [L0, L1), block by block.
 struct Walk {
@@ -340,8 +313,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mass_kernel(const __grid_const
                                           make_float2(cc.x, cc.y), make_float2(nn.x, nn.y));
               const float2 y = __ffma2_rn(__fmul2_rn(make_float2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), ks2),
                                           make_float2(cc.z, cc.w), make_float2(nn.z, nn.w));
-              sum = __fadd2_rn(sum, exp2_pair(x, (e / 2) % 8 < kPoly));
-              sum = __fadd2_rn(sum, exp2_pair(y, (e / 2 + 1) % 8 < kPoly));
+              sum = __fadd2_rn(sum, make_float2(ex2_approx(x.x), ex2_approx(x.y)));
+              sum = __fadd2_rn(sum, make_float2(ex2_approx(y.x), ex2_approx(y.y)));
             }
           };
           tmem_ld32(taddr, va);
