@@ -93,14 +93,14 @@ struct QFrag {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 f = unpack_bf16x2(u[e]);
-          if (fabsf(f.x) <= 3.4e38f) mx = fmaxf(mx, fabsf(f.x));
-          if (fabsf(f.y) <= 3.4e38f) mx = fmaxf(mx, fabsf(f.y));
+          mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
         }
       }
       mx = quad_max(mx);
       const int e = min(max(exponent_of(mx), -100), 126);
       const float down = pow2f(-e);
-      coef[i] = pow2f(e) * scale * kLog2e;
+      // an infinite element makes its row NaN, also where it would send every score to -inf
+      coef[i] = mx == INFINITY ? NAN : pow2f(e) * scale * kLog2e;
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) {
         // 8 channels: two MMA steps, (0,1) and (2,3) of each to their two halves
@@ -762,6 +762,9 @@ __global__ void __launch_bounds__(kF32Threads) q8_attend_f32_kernel(const Q8Atte
 #pragma unroll
     for (int r = 0; r < kF32Rows; ++r) {
       load_q<D>(static_cast<const float*>(a.Q) + (row0 + min(r, rows - 1)) * D + sub * (D / 8), a.scale * kLog2e, q[r]);
+      // an infinite element makes its row NaN, also where it would send every score to -inf
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k) q[r][k] = fabsf(q[r][k]) == INFINITY ? NAN : q[r][k];
       m[r] = -INFINITY;
       l[r] = 0.f;
 #pragma unroll

@@ -66,3 +66,22 @@ def test_mass_of_the_lowest_log_sums(dtype, rows):
             assert bool(torch.isposinf(c.mass[0, :500]).all())
             assert torch.equal(c.mass[1, :130], prev[1, :130])
         lse[0, at] = float("-inf")
+
+
+# ------------------------------------------------------------------ scores
+@pytest.mark.parametrize("dtype,rows", KERNELS)
+def test_attend_infinite_queries_against_one_sign(dtype, rows):
+    """An infinite element gives a NaN row also where it would send every score to -inf."""
+    import torch
+    torch.manual_seed(rows)
+    dt = _dt(dtype)[0]
+    c = filled(1, 64, 256, 32, dtype, [200], 4, max_queries=rows)
+    c.K[0, :200, 9] = torch.tensor([-2.0]).to(torch.float8_e4m3fn).view(torch.uint8).cuda()
+    Q = torch.randn(1, rows, 64, device="cuda").to(dt)
+    clean, clean_lse = attend(c, Q)
+    at = rows // 2
+    Q[0, at, 9] = float("inf")
+    O, lse = attend(c, Q)
+    assert bool(O[0, at].isnan().all()) and bool(lse[0, at].isnan())
+    keep = torch.arange(rows, device="cuda") != at
+    assert torch.equal(O[0, keep], clean[0, keep]) and torch.equal(lse[0, keep], clean_lse[0, keep])
