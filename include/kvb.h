@@ -505,8 +505,8 @@ KVB_API kvb_status kvb_q8_append(const kvb_q8_cache* c, const void* K, int64_t k
  * two E4M3 parts of each element or as fp16 with a power of two per row, weights as
  * fp16, sums fp32 (elements below 2^-14 of their row's largest, or below 2^-114, lose
  * bits); f32 runs on CUDA cores (small problems).  Scores below fp32's range count as
- * -inf; infinite or NaN queries give NaN rows.  O and lse overlap nothing else of the
- * call. */
+ * -inf (a row with no others is zeros with lse -inf); infinite or NaN queries give NaN
+ * rows.  O and lse overlap nothing else of the call. */
 KVB_API kvb_status kvb_q8_attend(const kvb_q8_cache* c, const void* Q, int32_t Nq, kvb_dtype dtype, float scale,
                                  void* O, float* lse, void* workspace, size_t workspace_bytes, void* stream);
 

@@ -79,6 +79,9 @@ __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) 
 // floor(log2 |x|) of a normal float; -126 or less for zero and subnormals
 __device__ __forceinline__ int exponent_of(float x) { return static_cast<int>((__float_as_uint(x) >> 23) & 0xFFu) - 127; }
 
+// what a row's sum divides its outputs by: a row that saw nothing, its every score -inf, is zeros
+__device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.f / l; }
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

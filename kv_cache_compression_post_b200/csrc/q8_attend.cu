@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const __grid_con
       tc_fence_after();
       __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.O) + row * D;
       if (pc.npieces == 1) {
-        const float inv = 1.f / l;
+        const float inv = inverse_sum(l);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t v[32];
@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const __grid_con
         for (int u = 0; u < kAhead; ++u)
           if (k0 + u < pc.npieces) L = fmaf(y[u], ex2_approx(x[u] - M), L);
       }
-      const float inv = 1.f / L;
+      const float inv = inverse_sum(L);
 #pragma unroll 1
       for (int c4 = 0; c4 < D / 4; c4 += 4) {
         float4 acc[4];

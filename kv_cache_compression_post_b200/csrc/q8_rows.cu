@@ -534,7 +534,7 @@ __device__ void finish_unit(const Q8AttendArgs& a, const Q8Piece& pc, size_t row
     L = warp_sum(L);
     __syncwarp();
     if (lane == 0) {
-      l[0] = 1.f / L;
+      l[0] = inverse_sum(L);
       if (a.lse) a.lse[row0 + row] = (M - bias + log2f(L)) * kLn2;
     }
   }
@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(Acc::kThreads, 1) q8_attend_rows_kernel(const 
         sum.w = fmaf(f, x.w, sum.w);
       }
       if (pc.npieces == 1) {
-        const float inv = 1.f / L;
+        const float inv = inverse_sum(L);
         put_row4<__nv_bfloat16, D>(a.O, row0 + row, c, make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv));
         if (a.lse && c == 0) a.lse[row0 + row] = (M - Acc::kBias + log2f(L)) * kLn2;
       } else {
@@ -824,7 +824,7 @@ __global__ void __launch_bounds__(kF32Threads) q8_attend_f32_kernel(const Q8Atte
         v = fmaf(f, so[(static_cast<size_t>(w) * kF32Rows + row) * D + c], v);
       }
       if (pc.npieces == 1) {
-        static_cast<float*>(a.O)[(row0 + row) * D + c] = v / L;
+        static_cast<float*>(a.O)[(row0 + row) * D + c] = L == 0.f ? 0.f : v / L;
         if (a.lse && c == 0) a.lse[row0 + row] = (M + log2f(L)) * kLn2;
       } else {
         slot[row * D + c] = v;

@@ -16,6 +16,34 @@ pytestmark = pytest.mark.gpu
 KERNELS = [("bf16", 1), ("bf16", 8), ("bf16", 12), ("bf16", 40), ("bf16", 100), ("bf16", 300), ("f32", 1), ("f32", 5)]
 
 
+def attend_one_head(c, h, Q, rows=None):
+    """(q, O, lse, size) of head h in fp64 (rows: those of them)."""
+    q = Q[h, slice(None) if rows is None else rows].double().cpu().numpy()
+    K, V = head_values(c, h)
+    sc = 1.0 / np.sqrt(Q.shape[2])
+    dS = (np.abs(q) @ np.abs(K).T).max(1, keepdims=True) * sc * 2.0 ** -17
+    return (*q8.attend(q, K, V, sc), dS)
+
+
+def check_rows(O, lse, ref, rows, dt, lost=0.0, dS_more=0.0):
+    """One head's outputs against attend_one_head's; `lost`: what else they may be off by, `dS_more`:
+    what else a score may be."""
+    import torch
+    want, want_lse, size, dS = ref
+    dS = dS + dS_more
+    pick = slice(None) if rows is None else rows
+    half = torch.finfo(dt).eps / 2
+    rel = 4 * dS + 2.0 ** -11 + 2.0 ** -18
+    tol = rel * size + lost
+    tol = tol + half * (np.abs(want) + tol)
+    err = np.abs(O[pick].double().cpu().numpy() - want)
+    assert np.all(err <= tol), float((err / tol).max())
+    if lse is not None:
+        el = np.abs(lse[pick].double().cpu().numpy() - want_lse)
+        tl = dS[:, 0] + 2.0 ** -18 + 2.0 ** -17 * (1 + np.abs(want_lse))
+        assert np.all(el <= tl), float((el / tl).max())
+
+
 # ------------------------------------------------------------------ weights
 @pytest.mark.parametrize("dtype,rows", KERNELS)
 @pytest.mark.parametrize("below", [60.0, 80.0, 200.0])
@@ -69,6 +97,31 @@ def test_mass_of_the_lowest_log_sums(dtype, rows):
 
 
 # ------------------------------------------------------------------ scores
+@pytest.mark.parametrize("dtype,rows", KERNELS + [("bf16", 70)])
+@pytest.mark.parametrize("n", [40, 30000])
+def test_attend_every_score_past_the_range_of_floats(n, dtype, rows):
+    """Scores below -2^128 count as -inf.  Rows with no other see nothing: zeros and lse -inf,
+    whole or cut into pieces; rows of the other head are untouched."""
+    import torch
+    torch.manual_seed(rows)
+    dt, cap = _dt(dtype)[0], -(-n // 64) * 64
+    c = filled(2, 128, cap, 64, dtype, [n, n - 7], 3, max_queries=rows)
+    lo = -2.0 ** 126
+    c.K[0, :n] = 0
+    c.K[0, :n, 0] = torch.tensor([lo * 2.0 ** -119]).to(torch.float8_e4m3fn).view(torch.uint8).cuda()
+    c.k_scale[0, :-(-n // 64)] = 2.0 ** 119
+    Q = torch.randn(2, rows, 128, device="cuda").to(dt)
+    Q[0, :, 0] = 64.0
+    O, lse = attend(c, Q)
+    assert c.status() == 0
+    assert bool((O[0] == 0).all()) and bool(torch.isneginf(lse[0]).all())
+    pick = None if n < 100 else np.array([0, rows - 1])
+    K, V = head_values(c, 1)
+    assert np.isfinite(K).all()
+    ref = attend_one_head(c, 1, Q, pick)
+    check_rows(O[1], lse[1], ref, pick, dt)
+
+
 @pytest.mark.parametrize("dtype,rows", KERNELS)
 def test_attend_infinite_queries_against_one_sign(dtype, rows):
     """An infinite element gives a NaN row also where it would send every score to -inf."""
