@@ -444,7 +444,7 @@ KVB_API kvb_status kvb_rope(const void* X, const int32_t* pos, int32_t heads, in
  * max|x| / scale <= 448 over the block, so scaling loses nothing and the only
  * rounding is E4M3's (step 2^-3 of a value's binade, above 2^-15 of the block's
  * largest); a block of zeros has 2^-100.  The attention and weight kernels accept any
- * positive finite scale; the V scales of a head have to lie within 2^100 of one another
+ * positive normal scale; the V scales of a head have to lie within 2^100 of one another
  * (bf16 attention leaves out tokens whose weight times V scale is below about 2^-130
  * of the largest).
  *

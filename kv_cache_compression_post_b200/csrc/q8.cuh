@@ -79,6 +79,10 @@ __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) 
 // floor(log2 |x|) of a normal float; -126 or less for zero and subnormals
 __device__ __forceinline__ int exponent_of(float x) { return static_cast<int>((__float_as_uint(x) >> 23) & 0xFFu) - 127; }
 
+// The row sums add weights / V scale, which passes fp32's range where a head's scales are
+// small (zeros have 2^-100; a million of them did).  They count in units of the power of two
+// of the head's first scale: an exact factor, taken out of outputs and lse in the end.
+__device__ __forceinline__ int sum_unit(const float* vs) { return min(max(exponent_of(__ldg(vs)), -126), 126); }
 // what a row's sum divides its outputs by: a row that saw nothing, its every score -inf, is zeros
 __device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.f / l; }
 

@@ -14,7 +14,8 @@
 // also makes P eight times more exact than a bf16 kernel's.
 // Scales: K's block scale multiplies a 16-token chunk's scores inside the FFMA that
 // feeds the exponential; V's rides in the exponent, P' = 2^(x + log2 vs - m + kPBias)
-// with m the running maximum of x + log2 vs, and the row sum adds P' / vs per chunk.
+// with m the running maximum of x + log2 vs, and the row sum adds P' / vs per chunk (in units
+// of sum_unit).
 // Neither costs an instruction per score.
 //
 // Work: units of (head, pair of 128-query tiles A, B), split over a persistent grid at
@@ -153,7 +154,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const __grid_con
   __shared__ Q8Sched sch;
   __shared__ Q8Walk s_it[8];
   __shared__ Q8Piece s_pc[8];
-  // per ring slot: K scales, log2 of V's and their reciprocals, of eight 16-token chunks
+  // per ring slot: K scales, log2 of V's and their reciprocals (in the sums' units), of eight
+  // 16-token chunks
   __shared__ alignas(16) float sScale[kScStages * 24];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const Q8AttendArgs& a = args.a;
@@ -279,6 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const __grid_con
           return lane < 16 ? __ldg(sp + (min(j * kTile + (lane & 7) * 16, n - 1) >> a.c.shift)) : 1.f;
         };
         float next = fetch(pc.j0);
+        const float per_unit = pow2f(-sum_unit(a.c.vs + static_cast<size_t>(pc.h) * blocks));
         for (int j = pc.j0; j < pc.j1; ++j, ++g) {
           const float s = next;
           if (j + 1 < pc.j1) next = fetch(j + 1);
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const __grid_con
             to[0] = s;
           } else if (lane < 16) {
             to[8] = lg2_approx(s);
-            to[16] = 1.f / s;
+            to[16] = 1.f / (s * per_unit);
           }
           __syncwarp();
           if (lane == 0) {
@@ -571,12 +574,13 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const __grid_con
         if (lane == 0) mbar_arrive(&bars->p_full[t]);
       }
       if (!ok) break;
+      const int unit = sum_unit(a.c.vs + static_cast<size_t>(pc.h) * (a.c.cap >> a.c.shift));
       if (!(ok = wait_warp(&bars->o_full[t], npt & 1))) break;
       ++npt;
       tc_fence_after();
       __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.O) + row * D;
       if (pc.npieces == 1) {
-        const float inv = inverse_sum(l);
+        const float inv = inverse_sum(l) * pow2f(unit);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t v[32];
@@ -594,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const __grid_con
             }
           }
         }
-        if (a.lse && qrow < a.Nq) a.lse[row] = (m - kPBias + log2f(l)) * kLn2;
+        if (a.lse && qrow < a.Nq) a.lse[row] = (m - (kPBias + unit) + log2f(l)) * kLn2;
         continue;
       }
       // a piece of a cut unit: O as [D/4][128] float4, so that neighbouring rows are
@@ -650,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const __grid_con
         for (int u = 0; u < kAhead; ++u)
           if (k0 + u < pc.npieces) L = fmaf(y[u], ex2_approx(x[u] - M), L);
       }
-      const float inv = inverse_sum(L);
+      const float inv = inverse_sum(L) * pow2f(unit);
 #pragma unroll 1
       for (int c4 = 0; c4 < D / 4; c4 += 4) {
         float4 acc[4];
@@ -687,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_attend_kernel(const __grid_con
                            pack_bf16x2(acc[c + 1].x, acc[c + 1].y), pack_bf16x2(acc[c + 1].z, acc[c + 1].w));
         }
       }
-      if (a.lse && qrow < a.Nq) a.lse[row] = (M - kPBias + log2f(L)) * kLn2;
+      if (a.lse && qrow < a.Nq) a.lse[row] = (M - (kPBias + unit) + log2f(L)) * kLn2;
     }
     // rows of heads without tokens: zeros (lse -inf), spread over the CTAs
     if (ok) {

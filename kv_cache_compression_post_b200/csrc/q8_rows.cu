@@ -22,8 +22,8 @@
 // Softmax in the log2 domain.  With ks, vs the scales of a token's block,
 //     x = (q.k) ks scale log2 e,   P = 2^(x + log2 vs - m + kBias),
 // m the running maximum of x + log2 vs: V's scale rides in the exponent at no cost,
-// P stays within fp16's range, and the row sum adds P / vs per block.  Sums,
-// maxima and partial outputs are fp32.
+// P stays within fp16's range, and the row sum adds P / vs per block (in units of
+// sum_unit).  Sums, maxima and partial outputs are fp32.
 #include "host_util.h"
 #include "q8.cuh"
 #include "sm100.cuh"
@@ -274,7 +274,7 @@ struct RowsShared {
   float m[WARPS][ROWS], l[WARPS][ROWS];
 };
 
-// The scales of 32 tokens' two halves: K's, log2 and reciprocal of V's
+// The scales of 32 tokens' two halves: K's, log2 and reciprocal (in the sums' units) of V's
 struct StepScales {
   float kf[2], lv[2], iv[2];
 };
@@ -484,11 +484,11 @@ __device__ __forceinline__ void put_row4(void* O, size_t row, int c, float4 v) {
 // A piece that finds all pieces of its unit there merges them, in their order: their maxima
 // and sums, fetched at once, become one weight per (row, piece), and weigh the outputs,
 // sixteen of which are on their way meanwhile.  (A second kernel for it cost 6 us.)  Called
-// by the whole CTA after it has stored its own piece; s_w, s_l: shared memory, ROWS x
-// kQ8MaxCtas each.
+// by the whole CTA after it has stored its own piece; unit: log2 of the sums' unit; s_w,
+// s_l: shared memory, ROWS x kQ8MaxCtas each.
 template <int D, typename T, int ROWS>
-__device__ void finish_unit(const Q8AttendArgs& a, const Q8Piece& pc, size_t row0, int rows, float bias, float* s_w,
-                            float* s_l, int* s_last) {
+__device__ void finish_unit(const Q8AttendArgs& a, const Q8Piece& pc, size_t row0, int rows, float bias, int unit,
+                            float* s_w, float* s_l, int* s_last) {
   const int tid = threadIdx.x, nthreads = blockDim.x, np = pc.npieces;
   __threadfence();
   __syncthreads();
@@ -534,8 +534,8 @@ __device__ void finish_unit(const Q8AttendArgs& a, const Q8Piece& pc, size_t row
     L = warp_sum(L);
     __syncwarp();
     if (lane == 0) {
-      l[0] = inverse_sum(L);
-      if (a.lse) a.lse[row0 + row] = (M - bias + log2f(L)) * kLn2;
+      l[0] = inverse_sum(L) * pow2f(unit);
+      if (a.lse) a.lse[row0 + row] = (M - (bias + unit) + log2f(L)) * kLn2;
     }
   }
   __syncthreads();
@@ -627,6 +627,7 @@ __global__ void __launch_bounds__(Acc::kThreads, 1) q8_attend_rows_kernel(const 
       }
     };
     scales(first);
+    const int unit = sum_unit(vs);
     if (sch.chunk == 0) q8_unit_pieces(S, pc.h, pc.r, pc);
     acc.begin(a.scale, t);
     int stage = 0;
@@ -646,7 +647,7 @@ __global__ void __launch_bounds__(Acc::kThreads, 1) q8_attend_rows_kernel(const 
       for (int u = 0; u < 2; ++u) {
         sc.kf[u] = nk[u];
         sc.lv[u] = log2f(nv[u]);
-        sc.iv[u] = 1.f / nv[u];
+        sc.iv[u] = 1.f / (nv[u] * pow2f(-unit));
       }
       if (kb + kHop < end) scales(kb + kHop);
       acc.step(kw, ring + stage * kStage + 32 * D, sc, kb, end, g, t);
@@ -676,9 +677,9 @@ __global__ void __launch_bounds__(Acc::kThreads, 1) q8_attend_rows_kernel(const 
         sum.w = fmaf(f, x.w, sum.w);
       }
       if (pc.npieces == 1) {
-        const float inv = inverse_sum(L);
+        const float inv = inverse_sum(L) * pow2f(unit);
         put_row4<__nv_bfloat16, D>(a.O, row0 + row, c, make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv));
-        if (a.lse && c == 0) a.lse[row0 + row] = (M - Acc::kBias + log2f(L)) * kLn2;
+        if (a.lse && c == 0) a.lse[row0 + row] = (M - (Acc::kBias + unit) + log2f(L)) * kLn2;
       } else {
         *reinterpret_cast<float4*>(slot + row * D + c) = sum;
         if (c == 0) {
@@ -690,7 +691,7 @@ __global__ void __launch_bounds__(Acc::kThreads, 1) q8_attend_rows_kernel(const 
     if (pc.npieces > 1) {
       __syncthreads();  // the warps' outputs have been read
       float* s_w = reinterpret_cast<float*>(smem);
-      finish_unit<D, __nv_bfloat16, kTileRows>(a, pc, row0, rows, Acc::kBias, s_w, s_w + kTileRows * kQ8MaxCtas, &s_last);
+      finish_unit<D, __nv_bfloat16, kTileRows>(a, pc, row0, rows, Acc::kBias, unit, s_w, s_w + kTileRows * kQ8MaxCtas, &s_last);
     }
     __syncthreads();  // the merge is done with the shared memory
   }
@@ -836,7 +837,7 @@ __global__ void __launch_bounds__(kF32Threads) q8_attend_f32_kernel(const Q8Atte
     }
     if (pc.npieces > 1) {
       __syncthreads();  // the groups' outputs have been read
-      finish_unit<D, float, kF32Rows>(a, pc, row0, rows, 0.f, so, so + kF32Rows * kQ8MaxCtas, &s_last);
+      finish_unit<D, float, kF32Rows>(a, pc, row0, rows, 0.f, 0, so, so + kF32Rows * kQ8MaxCtas, &s_last);
     }
     __syncthreads();  // the merge is done with the shared memory
   }

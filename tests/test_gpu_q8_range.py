@@ -8,7 +8,7 @@ import numpy as np
 import pytest
 
 from oracle import q8cache as q8
-from tests.test_gpu_q8 import _dt, attend, check_mass, filled, head_values
+from tests.test_gpu_q8 import _dt, attend, check_attend, check_mass, filled, head_values, poisoned
 
 pytestmark = pytest.mark.gpu
 
@@ -138,3 +138,60 @@ def test_attend_infinite_queries_against_one_sign(dtype, rows):
     assert bool(O[0, at].isnan().all()) and bool(lse[0, at].isnan())
     keep = torch.arange(rows, device="cuda") != at
     assert torch.equal(O[0, keep], clean[0, keep]) and torch.equal(lse[0, keep], clean_lse[0, keep])
+
+
+# ------------------------------------------------------------------ V scales
+@pytest.mark.parametrize("dtype,rows", KERNELS)
+@pytest.mark.parametrize("exp", [-122, -100, 100])
+def test_attend_scales_of_any_size(exp, dtype, rows):
+    """V scales far from 1, also below the smallest that an append writes."""
+    import torch
+    torch.manual_seed(rows)
+    c = filled(2, 128, 512, 16, dtype, [500, 77], 2, max_queries=rows)
+    c.v_scale *= 2.0 ** (exp + 6)
+    Q = (2 * torch.randn(2, rows, 128, device="cuda")).to(_dt(dtype)[0])
+    O, lse = attend(c, Q)
+    assert c.status() == 0
+    check_attend(c, Q, O, lse)
+
+
+@pytest.mark.parametrize("dtype,rows", KERNELS)
+@pytest.mark.parametrize("first", [True, False])
+def test_attend_blocks_of_zeros_among_others(first, dtype, rows):
+    """Zero blocks as an append writes them (scale 2^-100) at the head's start or behind others:
+    their tokens weigh as much as the rest."""
+    import torch
+    torch.manual_seed(rows)
+    n, dt = 500, _dt(dtype)[0]
+    c = poisoned(2, 64, 512, 16, dtype, max_queries=rows)
+    K, V = torch.randn(2, 2, n, 64, device="cuda")
+    zero = (torch.arange(n, device="cuda") // 16) % 2 == (0 if first else 1)
+    V[0, zero] = 0
+    V[1, zero] = 0
+    V[1] *= 2.0 ** 6                        # scales 2^100 apart
+    c.append(K.to(dt), V.to(dt))
+    assert float(c.v_scale[0, 0 if first else 1]) == 2.0 ** -100
+    Q = torch.randn(2, rows, 64, device="cuda").to(dt)
+    O, lse = attend(c, Q)
+    check_attend(c, Q, O, lse)
+
+
+@pytest.mark.parametrize("dtype,rows", [("bf16", 1), ("bf16", 12), ("bf16", 60), ("bf16", 140), ("f32", 2)])
+def test_attend_millions_of_zeros(dtype, rows):
+    """A head of zeros, as appended, has a finite lse: 2^22 + 5 tokens."""
+    import torch
+    import kv_cache_compression_post_b200 as kvb
+    n = (1 << 22) + 5
+    c = kvb.Q8Cache(1, 64, n + 59, 64, dtype=_dt(dtype)[1], max_queries=rows)
+    c.K.zero_()
+    c.V.zero_()
+    c.k_scale.fill_(2.0 ** -100)
+    c.v_scale.fill_(2.0 ** -100)
+    c.len.fill_(n)
+    Q = torch.randn(1, rows, 64, device="cuda").to(_dt(dtype)[0])
+    O, lse = attend(c, Q)
+    assert c.status() == 0
+    assert bool((O == 0).all())
+    # a sum of up to 2000 equal terms a lane, 200 sums merged: 2200 roundings of 2^-24 at most, and
+    # the roundings of a log sum put together from terms of about 100: 2^-16
+    assert float((lse.double() - np.log(n)).abs().max()) <= 2200 * 2.0 ** -24 + 2.0 ** -15
