@@ -493,7 +493,8 @@ KVB_API size_t kvb_q8_workspace_size(const kvb_q8_cache* c, int32_t max_queries,
  * set to 0 for the new tokens.  A head without room (start[h] < 0 or start[h] + n >
  * capacity) is left as it was, and KVB_E_DEVICE_BOUNDS goes to the status word.
  * Values beyond 448 * 2^119 saturate, infinities become +-448 codes and take no part
- * in the scale, NaN stays NaN.  n >= 0; n == 0 with start NULL does nothing. */
+ * in the scale, NaN stays NaN.  0 <= n <= capacity; n == 0 moves the lengths to `start`
+ * and nothing else (start NULL: nothing). */
 KVB_API kvb_status kvb_q8_append(const kvb_q8_cache* c, const void* K, int64_t k_head_stride, int64_t k_token_stride,
                                  const void* V, int64_t v_head_stride, int64_t v_token_stride, int32_t n,
                                  kvb_dtype dtype, const int32_t* start, void* stream);

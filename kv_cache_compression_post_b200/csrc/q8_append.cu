@@ -173,7 +173,8 @@ __global__ void __launch_bounds__(2 * kHalf) q8_append_few_kernel(const Q8Append
     if (threadIdx.x == 0) latch_status(a.status, KVB_E_DEVICE_BOUNDS);
     return;
   }
-  for (int b = start / a.block; b * a.block < start + a.n; ++b)
+  // (an empty run touches no block, also where it starts inside one)
+  for (int b = start / a.block; a.n > 0 && b * a.block < start + a.n; ++b)
     append_block<T, CH>(a, kv, h, b, start, tid, 1 + kv, s_max[kv]);
   __syncthreads();  // every thread has read start, which may be this word
   if (threadIdx.x == 0) a.len[h] = start + a.n;

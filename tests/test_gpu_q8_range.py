@@ -195,3 +195,22 @@ def test_attend_millions_of_zeros(dtype, rows):
     # a sum of up to 2000 equal terms a lane, 200 sums merged: 2200 roundings of 2^-24 at most, and
     # the roundings of a log sum put together from terms of about 100: 2^-16
     assert float((lse.double() - np.log(n)).abs().max()) <= 2200 * 2.0 ** -24 + 2.0 ** -15
+
+
+# ------------------------------------------------------------------ append
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_append_of_nothing_moves_only_the_length(dtype):
+    """A start inside a block whose scale lies below what an append would write."""
+    import torch
+    H, d, block = 3, 64, 16
+    c = filled(H, d, 64, block, dtype, [40] * H, 3)
+    for s in (c.k_scale, c.v_scale):
+        s[:, :3] = 2.0 ** -120
+    before = [t.clone() for t in (c.K, c.V, c.k_scale, c.v_scale, c.mass)]
+    empty = torch.empty(H, 0, d, device="cuda", dtype=_dt(dtype)[0])
+    c.append(empty, empty, start=torch.tensor([37, 5, 64], dtype=torch.int32, device="cuda"))
+    assert c.len.tolist() == [37, 5, 64] and c.status() == 0
+    for t, b in zip((c.K, c.V, c.k_scale, c.v_scale, c.mass), before):
+        assert torch.equal(t.view(torch.uint8), b.view(torch.uint8))
+    c.append(empty, empty, start=torch.tensor([-1, 65, 7], dtype=torch.int32, device="cuda"))
+    assert c.len.tolist() == [37, 5, 7] and c.status() == 5
