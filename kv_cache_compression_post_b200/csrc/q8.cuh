@@ -328,8 +328,9 @@ struct Q8ChunkScratch {
   unsigned int* cnt;     // [H][pairs of query tiles][2], or kQ8MassCounters
 };
 inline size_t q8_chunk_part_floats(int d) { return static_cast<size_t>(4) * kQ8MaxCtas * (128 * d + 256); }
-cudaError_t launch_q8_split_q(const void* Q, long long rows, int d, float scale, const Q8ChunkScratch& s, int ncnt,
-                              int n_sm, cudaStream_t st);
+// lse: of the rows, or null; rows of -inf, which weigh nothing whatever they hold, become zeros
+cudaError_t launch_q8_split_q(const void* Q, const float* lse, long long rows, int d, float scale,
+                              const Q8ChunkScratch& s, int ncnt, int n_sm, cudaStream_t st);
 cudaError_t launch_q8_mass_chunk(const Q8MassArgs& a, const Q8ChunkScratch& s, int n_sm, cudaStream_t st);
 constexpr int kQ8MassCounters = kQ8MaxCtas * 2 * 8;  // arrival counters of the weights' cut blocks
 cudaError_t launch_q8_attend_chunk(const Q8AttendArgs& a, const Q8ChunkScratch& s, int n_sm, cudaStream_t st);

@@ -93,9 +93,9 @@ struct Args {
 // took 12).  Also zeroes the arrival counters of the launch that follows.
 constexpr int kSplitFlight = 4;
 template <int D>
-__global__ void __launch_bounds__(256) q8_split_q_kernel(const __nv_bfloat16* Q, long long rows, float scale,
-                                                         uint8_t* hi, uint8_t* lo, float* coef, unsigned int* cnt,
-                                                         int ncnt) {
+__global__ void __launch_bounds__(256) q8_split_q_kernel(const __nv_bfloat16* Q, const float* lse, long long rows,
+                                                         float scale, uint8_t* hi, uint8_t* lo, float* coef,
+                                                         unsigned int* cnt, int ncnt) {
   pdl_wait();
   pdl_trigger();
   const long long gt = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
@@ -105,14 +105,17 @@ __global__ void __launch_bounds__(256) q8_split_q_kernel(const __nv_bfloat16* Q,
   const int lane = threadIdx.x & 31, c = lane % kLanes;
   for (long long r0 = (gt >> 5) * (kPer * kSplitFlight); r0 < rows; r0 += (nt >> 5) * (kPer * kSplitFlight)) {
     uint4 w[kSplitFlight];
+    float z[kSplitFlight];
 #pragma unroll
     for (int u = 0; u < kSplitFlight; ++u) {
       const long long row = r0 + u * kPer + lane / kLanes;
       w[u] = row < rows ? __ldg(reinterpret_cast<const uint4*>(Q + row * D) + c) : make_uint4(0u, 0u, 0u, 0u);
+      z[u] = lse && row < rows ? __ldg(lse + row) : 0.f;
     }
 #pragma unroll
     for (int u = 0; u < kSplitFlight; ++u) {
       const long long row = r0 + u * kPer + lane / kLanes;
+      if (z[u] == -INFINITY) w[u] = make_uint4(0u, 0u, 0u, 0u);
       const uint32_t v[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
       float f[8], mx = 0.f;
 #pragma unroll
@@ -741,7 +744,7 @@ cudaError_t launch(const Q8AttendArgs& a, const Q8ChunkScratch& s, int n_sm, cud
   e = cudaFuncGetAttributes(&fa, q8_attend_kernel<D>);
   if (e != cudaSuccess) return e;
   if (fa.numRegs * 4 < kRegsControl + kRegsWiden + 2 * kRegsSoftmax) return cudaErrorLaunchOutOfResources;
-  e = launch_q8_split_q(a.Q, rows, D, a.scale, s, a.c.H * npair * 2, n_sm, st);
+  e = launch_q8_split_q(a.Q, nullptr, rows, D, a.scale, s, a.c.H * npair * 2, n_sm, st);
   if (e != cudaSuccess) return e;
   Args args{a, s.coef, s.cnt};
   args.a.part = s.part;
@@ -752,16 +755,16 @@ cudaError_t launch(const Q8AttendArgs& a, const Q8ChunkScratch& s, int n_sm, cud
 
 }  // namespace
 
-cudaError_t launch_q8_split_q(const void* Q, long long rows, int d, float scale, const Q8ChunkScratch& s, int ncnt,
-                              int n_sm, cudaStream_t st) {
+cudaError_t launch_q8_split_q(const void* Q, const float* lse, long long rows, int d, float scale,
+                              const Q8ChunkScratch& s, int ncnt, int n_sm, cudaStream_t st) {
   const long long per = 8 * (256 / d) * kSplitFlight, need = (rows + per - 1) / per;  // rows of a CTA
   const int grid = static_cast<int>(need < 16LL * n_sm ? need : 16LL * n_sm);
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(Q);
   LaunchTrace trace("q8_split_q_kernel", st);
-  return d == 128 ? launch_pdl(q8_split_q_kernel<128>, dim3(grid), dim3(256), 0, st, q, rows, scale, s.hi, s.lo, s.coef,
-                               s.cnt, ncnt)
-                  : launch_pdl(q8_split_q_kernel<64>, dim3(grid), dim3(256), 0, st, q, rows, scale, s.hi, s.lo, s.coef,
-                               s.cnt, ncnt);
+  return d == 128 ? launch_pdl(q8_split_q_kernel<128>, dim3(grid), dim3(256), 0, st, q, lse, rows, scale, s.hi, s.lo,
+                               s.coef, s.cnt, ncnt)
+                  : launch_pdl(q8_split_q_kernel<64>, dim3(grid), dim3(256), 0, st, q, lse, rows, scale, s.hi, s.lo,
+                               s.coef, s.cnt, ncnt);
 }
 
 cudaError_t launch_q8_attend_chunk(const Q8AttendArgs& a, const Q8ChunkScratch& s, int n_sm, cudaStream_t st) {

@@ -389,7 +389,7 @@ cudaError_t launch(const Q8MassArgs& a, const Q8ChunkScratch& s, int n_sm, cudaS
   constexpr size_t smem = 1024 + 2 * kRowTile * D + kStages * 2 * kCols * D + kBarBytes;
   cudaError_t e = cudaFuncSetAttribute(q8_mass_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  e = launch_q8_split_q(a.Q, static_cast<long long>(a.c.H) * a.Nq, D, a.scale, s, kQ8MassCounters, n_sm, st);
+  e = launch_q8_split_q(a.Q, a.lse, static_cast<long long>(a.c.H) * a.Nq, D, a.scale, s, kQ8MassCounters, n_sm, st);
   if (e != cudaSuccess) return e;
   const Args args{a, s.coef, s.part, s.cnt};
   LaunchTrace trace("q8_mass_kernel", st);

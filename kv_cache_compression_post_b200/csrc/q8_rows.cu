@@ -860,15 +860,23 @@ struct WeightRows {
     const size_t row0 = static_cast<size_t>(h) * a.Nq + r0;
     const int rows = min(kRows, a.Nq - r0);
     q.fetch(static_cast<const __nv_bfloat16*>(a.Q) + row0 * D, rows, g, t);
+    float zq[kI];  // of the fragments' rows
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = FEW ? 2 * t + i : g + 8 * i;
+    for (int i = 0; i < kI; ++i) {
+      const int row = g + 8 * i;
       const float v = row < rows ? a.lse[row0 + row] : -INFINITY;
-      z[i] = v == -INFINITY ? -INFINITY : -v * kLog2e;
+      zq[i] = v == -INFINITY ? -INFINITY : -v * kLog2e;
+      // whatever the queries of a row that weighs nothing hold, NaN say, stays out of the sums
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k)
+        if (v == -INFINITY) q.raw[i][k] = make_uint4(0u, 0u, 0u, 0u);
     }
     q.widen(a.scale);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) coef[i] = FEW ? __shfl_sync(0xffffffffu, q.coef[0], 4 * (2 * t + i)) : q.coef[i % kI];
+    for (int i = 0; i < 2; ++i) {
+      coef[i] = FEW ? __shfl_sync(0xffffffffu, q.coef[0], 4 * (2 * t + i)) : q.coef[i % kI];
+      z[i] = FEW ? __shfl_sync(0xffffffffu, zq[0], 4 * (2 * t + i)) : zq[i % kI];
+    }
   }
   // the weights of 32 tokens, summed over the rows; token mine(g, t) of them returned
   static __device__ __forceinline__ int mine(int g, int t) { return FEW ? 8 * t + g : 8 * (g >> 1) + 2 * t + (g & 1); }

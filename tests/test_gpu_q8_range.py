@@ -96,6 +96,31 @@ def test_mass_of_the_lowest_log_sums(dtype, rows):
         lse[0, at] = float("-inf")
 
 
+@pytest.mark.parametrize("dtype,rows", KERNELS)
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -3e38])
+def test_mass_of_padded_rows(value, dtype, rows):
+    """Rows of lse -inf weigh nothing, whatever their queries hold: what the others give alone."""
+    import torch
+    torch.manual_seed(rows)
+    c = filled(2, 128, 512, 64, dtype, [500, 77], rows, max_queries=rows)
+    Q = torch.randn(2, rows, 128, device="cuda").to(_dt(dtype)[0])
+    _, lse = attend(c, Q)
+    pad = torch.rand(2, rows, device="cuda") < 0.5
+    pad[0, rows // 2] = True
+    pad[1, 0] = False
+    lse[pad] = float("-inf")
+    prev = c.mass.clone()
+    Q[pad] = 0
+    c.accumulate(Q, lse, prev=prev)
+    want = c.mass.clone()
+    c.mass.copy_(prev)
+    Q[pad] = value
+    c.accumulate(Q, lse, prev=prev)
+    assert c.status() == 0
+    assert torch.equal(c.mass.view(torch.int32), want.view(torch.int32))
+    check_mass(c, torch.where(pad[..., None], torch.zeros_like(Q), Q), lse, 1.0, prev)
+
+
 # ------------------------------------------------------------------ scores
 @pytest.mark.parametrize("dtype,rows", KERNELS + [("bf16", 70)])
 @pytest.mark.parametrize("n", [40, 30000])
