@@ -444,9 +444,11 @@ KVB_API kvb_status kvb_rope(const void* X, const int32_t* pos, int32_t heads, in
  * max|x| / scale <= 448 over the block, so scaling loses nothing and the only
  * rounding is E4M3's (step 2^-3 of a value's binade, above 2^-15 of the block's
  * largest); a block of zeros has 2^-100.  The attention and weight kernels accept any
- * positive normal scale; the V scales of a head have to lie within 2^100 of one another
- * (bf16 attention leaves out tokens whose weight times V scale is below about 2^-130
- * of the largest).
+ * positive normal scale; the V scales of a head have to lie within 2^100 of one another.
+ * Sums of weights are fp32, but bf16 attention multiplies V by fp16 weights: a token's
+ * weight times V scale is good to 2^-11 of itself down to 2^-20 of the row's largest such
+ * product, to 2^-31 of the largest below that, and 0 from about there on.  Seen in a
+ * channel that only tokens so far down fill, V being zero there in the others.
  *
  * Sequences of a batch are further heads (heads = batch x K/V heads).  Query heads
  * that share a K/V head are further rows of it: [batch][Hq][n][d] queries are, as

@@ -22,8 +22,10 @@
 // Softmax in the log2 domain.  With ks, vs the scales of a token's block,
 //     x = (q.k) ks scale log2 e,   P = 2^(x + log2 vs - m + kBias),
 // m the running maximum of x + log2 vs: V's scale rides in the exponent at no cost,
-// P stays within fp16's range, and the row sum adds P / vs per block (in units of
-// sum_unit).  Sums, maxima and partial outputs are fp32.
+// P stays below fp16's largest, and the row sum adds P / vs per block (in units of
+// sum_unit).  Sums, maxima and partial outputs are fp32.  P is rounded to fp16: its 11 bits
+// hold down to 2^-14, 2^-20 of the largest P or less, its smallest steps (2^-24) below that;
+// bf16 would hold any, with 8 bits of each.
 #include "host_util.h"
 #include "q8.cuh"
 #include "sm100.cuh"

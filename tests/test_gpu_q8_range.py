@@ -2,13 +2,17 @@
 far from 1, weights too small for the 16 bits they are held in.
 
 Tolerances are those of test_gpu_q8.py (a score is off by dS, a weight by a factor
-1 + rel), widened where a test says so.
+1 + rel), widened where a test says so:
+
+* A weight times its token's V scale is held in fp16 with the row's largest at 2^6 or more:
+  below 2^-20 of the largest it is subnormal there, off by at most half a step, 2^-25, or
+  2^-31 of the largest.
 """
 import numpy as np
 import pytest
 
 from oracle import q8cache as q8
-from tests.test_gpu_q8 import _dt, attend, check_attend, check_mass, filled, head_values, poisoned
+from tests.test_gpu_q8 import _dt, attend, check_attend, check_mass, filled, head_values, host_codes, poisoned
 
 pytestmark = pytest.mark.gpu
 
@@ -239,3 +243,38 @@ def test_append_of_nothing_moves_only_the_length(dtype):
         assert torch.equal(t.view(torch.uint8), b.view(torch.uint8))
     c.append(empty, empty, start=torch.tensor([-1, 65, 7], dtype=torch.int32, device="cuda"))
     assert c.len.tolist() == [37, 5, 7] and c.status() == 5
+
+
+# ------------------------------------------------------------------ small weights
+@pytest.mark.parametrize("dtype,rows", KERNELS)
+@pytest.mark.parametrize("apart", [12, 19, 20, 23, 27, 30, 33, 40])
+def test_attend_channels_only_small_scales_fill(apart, dtype, rows):
+    """Blocks of large V scale that are zero in half of the channels: the others come from tokens
+    whose weight times scale is 2^-apart of the largest.  Full precision down to 2^-20, then
+    what the smallest 16-bit weights hold (f32: all of it)."""
+    import torch
+    torch.manual_seed(apart)
+    n, d, dt = 480, 64, _dt(dtype)[0]
+    c = filled(1, d, 512, 16, dtype, [n], 5, max_queries=rows, spread=False)
+    big = (torch.arange(n, device="cuda") // 16) % 3 == 0
+    c.V[0, :n][big, d // 2:] = 0
+    c.V[0, :n][~big, :d // 2] = 0
+    c.v_scale[0, :n // 16] = torch.where(big[::16], 1.0, 2.0 ** -apart)
+    c.K[0, :n] = 0                          # scores in one channel: 0 to 1/4, so that weights are not powers of two
+    c.K[0, :n, 0] = (torch.rand(n, device="cuda") * 2).to(torch.float8_e4m3fn).view(torch.uint8)
+    c.k_scale[0, :n // 16] = 1.0
+    Q = torch.zeros(1, rows, d, dtype=dt, device="cuda")
+    Q[0, :, 0] = torch.rand(rows, device="cuda").to(dt)
+    O, lse = attend(c, Q)
+    assert c.status() == 0
+    ref = attend_one_head(c, 0, Q)
+    K, V = head_values(c, 0)
+    q = Q[0].double().cpu().numpy()
+    w = np.exp(q @ K.T / np.sqrt(d))
+    w /= w.sum(1, keepdims=True)
+    scale = np.repeat(c.v_scale[0, :n // 16].double().cpu().numpy(), 16)
+    codes = np.abs(host_codes(c.V[0, :n]))
+    lost = 0.0
+    if dtype == "bf16" and apart >= 20:
+        lost = 2.0 ** -31 * (w * scale).max(1, keepdims=True) * codes.sum(0, keepdims=True)
+    check_rows(O[0], lse[0], ref, None, dt, lost=lost)
