@@ -505,18 +505,21 @@ KVB_API kvb_status kvb_q8_append(const kvb_q8_cache* c, const void* K, int64_t k
  * [heads][Nq][d] of `dtype`, 16-byte aligned; lse: device [heads][Nq] f32 (natural
  * log of the sum of exp(scale q.k)) or NULL; scale > 0, or 0 => 1/sqrt(d).  One query
  * (a single token) up to whole chunks.  bf16 runs on the tensor cores: Q enters as
- * two E4M3 parts of each element or as fp16 with a power of two per row, weights as
- * fp16, sums fp32 (elements below 2^-14 of their row's largest, or below 2^-114, lose
- * bits); f32 runs on CUDA cores (small problems).  Scores below fp32's range count as
- * -inf (a row with no others is zeros with lse -inf); infinite or NaN queries give NaN
- * rows.  O and lse overlap nothing else of the call. */
+ * fp16 with a power of two per row (elements below 2^-14 of their row's largest lose
+ * bits) or, tens of rows and more, as two E4M3 parts of each element (whole down to 2^-9
+ * of the row's largest, below that off by at most 2^-17 of the largest: a channel far
+ * above the others costs these bits, felt where K is small in it); elements below 2^-114
+ * lose bits in either; weights are fp16, sums fp32.  f32 runs on CUDA cores (small
+ * problems).  Scores below fp32's range count as -inf (a row with no others is zeros with
+ * lse -inf); infinite or NaN queries give NaN rows.  O and lse overlap nothing else of
+ * the call. */
 KVB_API kvb_status kvb_q8_attend(const kvb_q8_cache* c, const void* Q, int32_t Nq, kvb_dtype dtype, float scale,
                                  void* O, float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 /* The attention weight each held token received from these queries:
  *   mass[h][k] = decay * prev[h][k] + sum_r exp(scale q_r.k - lse[h][r])
  * with lse as kvb_q8_attend returned it (rows of lse -inf weigh nothing, whatever their
- * queries hold).  prev: device [heads][capacity] f32, NULL (taken as 0) or the cache's
+ * queries hold) and Q held as there.  prev: device [heads][capacity] f32, NULL (taken as 0) or the cache's
  * own `mass`; other overlaps with it are not allowed.  c->mass is required
  * (KVB_E_INVAL).  Sums run in a fixed order: equal inputs give equal bits. */
 KVB_API kvb_status kvb_q8_mass(const kvb_q8_cache* c, const void* Q, int32_t Nq, kvb_dtype dtype, float scale,

@@ -3,8 +3,9 @@
 //
 // The codes are multiplied as they lie.  A bf16 query element has 8 significant bits
 // and E4M3 holds 4, so with the row scaled by a power of two to a largest element in
-// [2^7, 2^8) every element is the exact sum of two E4M3 parts, q = hi + lo, down to
-// 2^-17 of the row's largest:
+// [2^7, 2^8) an element is the exact sum of two E4M3 parts, q = hi + lo, down to 2^-9 of the
+// power of two below the row's largest (its last bit is then E4M3's smallest step, 2^-9);
+// smaller ones are off by half of that step, at most 2^-17 of the row's largest:
 //     S = hi K^T + lo K^T        2 x kind::f8f6f4, K the cache's bytes from TMA
 // which costs the tensor time of one bf16 product and never widens K.
 // P V cannot be split so cheaply (every weight would be rounded twice, by the warps

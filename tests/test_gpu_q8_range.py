@@ -7,6 +7,11 @@ Tolerances are those of test_gpu_q8.py (a score is off by dS, a weight by a fact
 * A weight times its token's V scale is held in fp16 with the row's largest at 2^6 or more:
   below 2^-20 of the largest it is subnormal there, off by at most half a step, 2^-25, or
   2^-31 of the largest.
+* In the kernel for chunks of queries a query element is two E4M3 parts, the row's largest
+  in [2^7, 2^8).  An element of exponent e has 8 bits down to 2^(e-7): the first part leaves a
+  multiple of that, at most 8 of them, which the second part holds if the steps it has at its
+  smallest, 2^-9, reach: e >= -2, elements down to 2^-9 of the power of two below the row's
+  largest.  Those below are off by half a step, 2^-10, at most 2^-17 of the row's largest.
 """
 import numpy as np
 import pytest
@@ -278,3 +283,30 @@ def test_attend_channels_only_small_scales_fill(apart, dtype, rows):
     if dtype == "bf16" and apart >= 20:
         lost = 2.0 ** -31 * (w * scale).max(1, keepdims=True) * codes.sum(0, keepdims=True)
     check_rows(O[0], lse[0], ref, None, dt, lost=lost)
+
+
+# ------------------------------------------------------------------ queries
+@pytest.mark.parametrize("dtype,rows", KERNELS)
+@pytest.mark.parametrize("above", [4, 8, 9, 12, 14])
+def test_queries_with_a_channel_far_above_the_rest(above, dtype, rows):
+    """One query channel 2^above over the rest, K zero in it, heads of one token, whose lse is
+    its score: elements down to 2^-9 of the largest enter a chunk whole, those of 16-row tiles
+    down to 2^-14."""
+    import torch
+    torch.manual_seed(above)
+    H, d, dt = 60, 128, _dt(dtype)[0]
+    c = filled(H, d, 64, 64, dtype, [1] * H, 5, max_queries=rows)
+    c.K[:, 0, 7] = 0
+    Q = torch.rand(H, rows, d, device="cuda") + 1           # [1, 2): exponent 0 (2 after rounding up)
+    Q *= torch.where(torch.rand(H, rows, d, device="cuda") < 0.5, -1.0, 1.0)
+    Q[:, :, 7] = 2.0 ** above
+    Q = Q.to(dt)
+    O, lse = attend(c, Q)
+    assert c.status() == 0
+    chunk = dtype == "bf16" and rows >= 100
+    for h in range(H):
+        K, _ = head_values(c, h)
+        more = 0.0
+        if chunk and above > 9:
+            more = 2.0 ** (above - 17) * np.abs(K[0]).sum() / np.sqrt(d)
+        check_rows(O[h], lse[h], attend_one_head(c, h, Q), None, dt, dS_more=more)
