@@ -519,9 +519,9 @@ KVB_API kvb_status kvb_q8_attend(const kvb_q8_cache* c, const void* Q, int32_t N
 /* The attention weight each held token received from these queries:
  *   mass[h][k] = decay * prev[h][k] + sum_r exp(scale q_r.k - lse[h][r])
  * with lse as kvb_q8_attend returned it (rows of lse -inf weigh nothing, whatever their
- * queries hold) and Q held as there.  prev: device [heads][capacity] f32, NULL (taken as 0) or the cache's
- * own `mass`; other overlaps with it are not allowed.  c->mass is required
- * (KVB_E_INVAL).  Sums run in a fixed order: equal inputs give equal bits. */
+ * queries hold) and Q held as there.  prev: device [heads][capacity] f32, NULL (taken as
+ * 0) or the cache's own `mass`; other overlaps with it are not allowed.  c->mass is
+ * required (KVB_E_INVAL).  Sums run in a fixed order: equal inputs give equal bits. */
 KVB_API kvb_status kvb_q8_mass(const kvb_q8_cache* c, const void* Q, int32_t Nq, kvb_dtype dtype, float scale,
                                const float* lse, float decay, const float* prev, void* workspace,
                                size_t workspace_bytes, void* stream);

@@ -13,9 +13,9 @@
 // CTAs is summed, in order, by whichever warp comes last to its 32 keys.
 // What bounds it: exponentials.  A step is 65536 of them, 4096 clk at the unit's 16 per
 // clock and SM, against 2048 clk of tensor time (12 heads x 4680 queries x 15600 tokens:
-// 313 us; 16-row tiles on mma.sync took 2466).  One pair in eight as a polynomial on the FMA
-// pipe took 307 us, but its 2^n, put together from bits, is no infinity past 2^128, where a
-// caller's lse far below the scores leads.
+// 306 us; 16-row tiles on mma.sync took 2466).  One pair in eight as a polynomial on the FMA
+// pipe took 1 to 2 % less, but its 2^n, put together from bits, is no infinity past 2^128,
+// where a caller's lse far below the scores leads.
 // Warps: 0 loads, 1 MMA, 2 TMEM, 3 column coefficients, 4-11 epilogue of row tile 0,
 // 12-19 of row tile 1 (4 lane quarters x 2 column halves).
 #include "host_util.h"
@@ -309,10 +309,11 @@ __global__ void __launch_bounds__(kThreads, 1) q8_mass_kernel(const __grid_const
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
               const float4 cc = *reinterpret_cast<const float4*>(cf + k + e), nn = *reinterpret_cast<const float4*>(nl + k + e);
-              const float2 x = __ffma2_rn(__fmul2_rn(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), ks2),
-                                          make_float2(cc.x, cc.y), make_float2(nn.x, nn.y));
-              const float2 y = __ffma2_rn(__fmul2_rn(make_float2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), ks2),
-                                          make_float2(cc.z, cc.w), make_float2(nn.z, nn.w));
+              // the two scales first, as in the attention: a raw product times a key scale may pass fp32's range
+              const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])),
+                                          __fmul2_rn(make_float2(cc.x, cc.y), ks2), make_float2(nn.x, nn.y));
+              const float2 y = __ffma2_rn(make_float2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])),
+                                          __fmul2_rn(make_float2(cc.z, cc.w), ks2), make_float2(nn.z, nn.w));
               sum = __fadd2_rn(sum, make_float2(ex2_approx(x.x), ex2_approx(x.y)));
               sum = __fadd2_rn(sum, make_float2(ex2_approx(y.x), ex2_approx(y.y)));
             }

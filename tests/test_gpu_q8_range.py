@@ -310,3 +310,24 @@ def test_queries_with_a_channel_far_above_the_rest(above, dtype, rows):
         if chunk and above > 9:
             more = 2.0 ** (above - 17) * np.abs(K[0]).sum() / np.sqrt(d)
         check_rows(O[h], lse[h], attend_one_head(c, h, Q), None, dt, dS_more=more)
+
+
+# ------------------------------------------------------------------ K scales
+@pytest.mark.parametrize("dtype,rows", KERNELS)
+@pytest.mark.parametrize("exp", [-100, 112])
+def test_mass_of_far_key_scales(exp, dtype, rows):
+    """Keys and queries whose sizes make up for one another: scores and weights near 1."""
+    import torch
+    import kv_cache_compression_post_b200 as kvb
+    torch.manual_seed(rows)
+    n, d, dt = 300, 128, _dt(dtype)[0]
+    c = filled(1, d, 320, 64, dtype, [n], 2, max_queries=rows, spread=False)
+    c.K[0, :n] = (448 - 128 * torch.rand(n, d, device="cuda")).to(torch.float8_e4m3fn).view(torch.uint8)
+    c.k_scale[0, :5] = 2.0 ** exp
+    Q = (2.0 ** -min(exp, 100) * (1 + torch.rand(1, rows, d, device="cuda"))).to(dt)
+    scale = 2.0 ** (min(exp, 100) - exp - 17)
+    O, lse = attend(c, Q, scale)
+    check_attend(c, Q, O, lse, scale)
+    c.accumulate(Q, lse, prev=torch.zeros_like(c.mass), scale=scale)
+    assert c.status() == 0
+    check_mass(c, Q, lse, 1.0, torch.zeros_like(c.mass), scale)
