@@ -479,7 +479,7 @@ typedef struct {
 } kvb_q8_cache;
 
 /* Bytes of device scratch (256-byte aligned) the calls below need on this cache
- * for up to max_queries rows per head of this type; 0 if the sizes are invalid.
+ * for up to max_queries rows per head (1..2^30) of this type; 0 if the sizes are invalid.
  * Its contents need no initialisation and mean nothing between calls. */
 KVB_API size_t kvb_q8_workspace_size(const kvb_q8_cache* c, int32_t max_queries, kvb_dtype dtype);
 

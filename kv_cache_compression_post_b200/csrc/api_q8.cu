@@ -32,6 +32,9 @@ Q8View view(const kvb_q8_cache* c) {
   return Q8View{c->heads, c->head_dim, c->capacity, c->block, __builtin_ctz(c->block), c->K, c->V, c->k_scale, c->v_scale, c->len, c->status};
 }
 
+// rows per head of a call: sums of a row count and a tile stay below 2^31
+bool rows_ok(int32_t n) { return n >= 1 && n <= kQ8MaxRows; }
+
 bool dtype_ok(kvb_dtype t) { return t == KVB_BF16 || t == KVB_F32; }
 
 // One scratch serves every call on a cache: the row-tile kernels' piece flags, which
@@ -92,7 +95,7 @@ bool workspace_ok(const void* ws, size_t have, size_t want) { return ws && align
 extern "C" {
 
 size_t kvb_q8_workspace_size(const kvb_q8_cache* c, int32_t max_queries, kvb_dtype dtype) {
-  if (!sizes_ok(c) || (c->head_dim != 64 && c->head_dim != 128) || max_queries < 1 || !dtype_ok(dtype)) return 0;
+  if (!sizes_ok(c) || (c->head_dim != 64 && c->head_dim != 128) || !rows_ok(max_queries) || !dtype_ok(dtype)) return 0;
   return scratch(c, max_queries, dtype, nullptr).bytes;
 }
 
@@ -141,7 +144,7 @@ kvb_status kvb_q8_attend(const kvb_q8_cache* c, const void* Q, int32_t Nq, kvb_d
                          float* lse, void* workspace, size_t workspace_bytes, void* stream) {
   const kvb_status ok = check_cache(c);
   if (ok != KVB_OK) return ok;
-  if (Nq < 1 || !dtype_ok(dtype) || !(scale >= 0.f) || !std::isfinite(scale)) return KVB_E_INVAL;
+  if (!rows_ok(Nq) || !dtype_ok(dtype) || !(scale >= 0.f) || !std::isfinite(scale)) return KVB_E_INVAL;
   if (!Q || !O || !aligned(Q, 16) || !aligned(O, 16) || !aligned(lse, 4)) return KVB_E_INVAL;
   const Scratch s = scratch(c, Nq, dtype, workspace);
   if (!workspace_ok(workspace, workspace_bytes, s.bytes)) return KVB_E_WORKSPACE;
@@ -167,7 +170,8 @@ kvb_status kvb_q8_mass(const kvb_q8_cache* c, const void* Q, int32_t Nq, kvb_dty
                        float decay, const float* prev, void* workspace, size_t workspace_bytes, void* stream) {
   const kvb_status ok = check_cache(c);
   if (ok != KVB_OK) return ok;
-  if (Nq < 1 || !dtype_ok(dtype) || !(scale >= 0.f) || !std::isfinite(scale) || !std::isfinite(decay)) return KVB_E_INVAL;
+  if (!rows_ok(Nq) || !dtype_ok(dtype) || !(scale >= 0.f) || !std::isfinite(scale) || !std::isfinite(decay))
+    return KVB_E_INVAL;
   if (!Q || !lse || !c->mass || !aligned(Q, 16) || !aligned(lse, 4) || !aligned(prev, 4)) return KVB_E_INVAL;
   const Scratch s = scratch(c, Nq, dtype, workspace);
   if (!workspace_ok(workspace, workspace_bytes, s.bytes)) return KVB_E_WORKSPACE;

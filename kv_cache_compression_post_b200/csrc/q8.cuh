@@ -15,6 +15,7 @@ namespace kvb {
 
 constexpr int kQ8MaxHeads = 1024;
 constexpr int kQ8MaxCapacity = 1 << 24;
+constexpr int kQ8MaxRows = 1 << 30;
 constexpr int kQ8MaxCtas = 160;  // grid cap of the kernels that split work (>= the SMs of a B200)
 
 struct Q8View {
