@@ -74,8 +74,8 @@ Scratch scratch(const kvb_q8_cache* c, int32_t max_queries, kvb_dtype dtype, voi
 }
 
 // A tag that no other call of this process has, and that memory which was never written
-// by one holds with probability 2^-64 (the calls' count through a bijective mixing of
-// shifts and odd products).
+// by one holds with probability 2^-64: the calls' count through SplitMix64, whose steps are
+// bijective (Steele, Lea, Flood: Fast splittable pseudorandom number generators, 2014).
 unsigned long long next_tag() {
   static std::atomic<unsigned long long> calls{0};
   unsigned long long z = 0;
