@@ -418,10 +418,10 @@ KVB_API kvb_status kvb_segment_cosine(const void* K, const void* nextK, int32_t 
  *   out may equal X with equal strides; otherwise the two must not overlap, nor out's
  *   rows one another (a stride of 0 over several rows is KVB_E_INVAL; X's may be 0).
  * pos: device int32 [n_tokens][3].  axis_pairs: host int32[3], each >= 0, their
- *   sum <= head_dim / 2.  base > 0, finite.  heads 1..65535, n_tokens >= 0,
+ *   sum <= head_dim / 2.  base finite, at least 2^-21.  heads 1..65535, n_tokens >= 0,
  *   head_dim a multiple of 8 up to 256.
  * X, out and every stride (in bytes) must be multiples of 16 (KVB_E_INVAL).
- * Angles are formed and reduced in fp64, products and sums in fp32, one rounding
+ * Angles are formed (to 2^-45 of themselves) and reduced in fp64, products and sums in fp32, one rounding
  * to the output type. */
 typedef enum { KVB_ROPE_INTERLEAVED = 0, /* pair j = elements (2j, 2j+1) */
                KVB_ROPE_HALVES = 1       /* pair j = elements (j, j + head_dim/2) */

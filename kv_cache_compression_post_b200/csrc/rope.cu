@@ -205,7 +205,9 @@ extern "C" kvb_status kvb_rope(const void* X, const int32_t* pos, int32_t heads,
     return KVB_E_INVAL;
   if (dtype != KVB_BF16 && dtype != KVB_F32) return KVB_E_INVAL;
   if (pairing != KVB_ROPE_INTERLEAVED && pairing != KVB_ROPE_HALVES) return KVB_E_INVAL;
-  if (!axis_pairs || !(base > 0.f) || !std::isfinite(base)) return KVB_E_INVAL;
+  // from 2^-21 on angles stay below 2^52, where their reduction knows its whole turns; past
+  // that the remainder is no angle, and "sines" reached 10^11
+  if (!axis_pairs || !(base >= 0x1p-21f) || !std::isfinite(base)) return KVB_E_INVAL;
   long long pairs = 0;
   for (int i = 0; i < 3; ++i) {
     if (axis_pairs[i] < 0) return KVB_E_INVAL;
