@@ -337,18 +337,29 @@ constexpr int kQ8MassCounters = kQ8MaxCtas * 2 * 8;  // arrival counters of the 
 cudaError_t launch_q8_attend_chunk(const Q8AttendArgs& a, const Q8ChunkScratch& s, int n_sm, cudaStream_t st);
 
 // Rows per head from which a bf16 call takes the tcgen05 kernel (128 or 256 rows at once,
-// however few there are) instead of 16-row tiles, each of which reads the cache again:
-// more where the cache is so small that beginnings and merges are what takes time.
-// us measured, 16-row tiles / tcgen05, head_dim 128:
-//   attention   heads x tokens   32 rows     48 rows     64 rows     96 rows     128 rows
-//               12 x 15600       33 / 61     42 / 62     50 / 63     66 / 64     89 / 64
-//               8 x 131072       107 / 150   150 / 150   214 / 151   278 / 152   406 / 152
-//               1 x 8192         15 / 38     16 / 38     16 / 38     17 / 39     16 / 39
-//               64 x 1024        30 / 46     37 / 46     42 / 46     53 / 47     64 / 47
-//   weights     12 x 15600       20 / 28     26 / 29     32 / 29     44 / 29     55 / 29
-//               8 x 131072       74 / 113    101 / 114   127 / 114   180 / 114   234 / 114
-//               1 x 8192         7 / 11      7 / 11      7 / 11      9 / 11      11 / 11
-//               64 x 1024        9 / 18      11 / 18     13 / 18     17 / 18     22 / 18
+// however few there are) instead of 16-row tiles, each of which reads the cache again.  One
+// bound for attention and weights, by what the cache may hold (lengths are on the device):
+// it lies near the crossing of the weights, and of the attention with eight heads and more.
+// Few heads, whose long units a CTA alone merges in the tcgen05 kernel, cross later, at 112
+// (4 x 65536) to 384 rows (1 x 131072), and short caches at hundreds: there the bound costs
+// up to three times the tiles' time.  us of a captured call, 16-row tiles / tcgen05:
+//   head_dim 128  heads x tokens   32 rows    48 rows    64 rows    80 rows    96 rows    128 rows   256 rows
+//   attention     12 x 15616       36 / 61    45 / 61    53 / 61    69 / 60    70 / 60    93 / 61    164 / 72
+//                 24 x 15616       54 / 71    71 / 71    96 / 71    113 / 71   128 / 71   167 / 72   308 / 84
+//                 8 x 131072       113 / 151  159 / 151  227 / 150  294 / 150  296 / 150  429 / 150  790 / 175
+//                 1 x 131072       36 / 168   40 / 168   46 / 168   50 / 170   56 / 170   68 / 170   111 / 203
+//                 1 x 8192         15 / 40    15 / 41    15 / 40    16 / 41    16 / 41    16 / 41    20 / 43
+//                 64 x 1024        30 / 46    37 / 46    42 / 47    48 / 47    53 / 47    64 / 47    107 / 37
+//   weights       12 x 15616       20 / 29    25 / 29    30 / 29    35 / 29    40 / 29    50 / 29    91 / 30
+//                 8 x 131072       74 / 113   96 / 113   119 / 113  141 / 113  164 / 113  210 / 113  465 / 114
+//                 1 x 131072       14 / 22    17 / 23    20 / 23    24 / 23    27 / 23    34 / 23    61 / 25
+//                 1 x 8192         4 / 10     5 / 10     6 / 10     7 / 10     8 / 10     10 / 10    17 / 11
+//                 64 x 1024        9 / 18     10 / 18    12 / 18    14 / 18    16 / 18    20 / 18    34 / 19
+//   head_dim 64
+//   attention     12 x 15616       23 / 46    28 / 45    34 / 46    43 / 46    44 / 46    58 / 47    100 / 53
+//                 8 x 131072       69 / 117   96 / 118   137 / 118  178 / 118  178 / 118  259 / 119  448 / 138
+//   weights       12 x 15616       14 / 27    18 / 28    21 / 28    25 / 28    28 / 28    35 / 28    62 / 29
+//                 8 x 131072       54 / 109   68 / 110   82 / 111   96 / 111   110 / 111  139 / 111  260 / 111
 inline int q8_chunk_rows(long long heads, long long capacity) { return heads * capacity <= 131072 ? 81 : 49; }
 
 struct Q8EvictArgs {
