@@ -331,3 +331,44 @@ def test_mass_of_far_key_scales(exp, dtype, rows):
     c.accumulate(Q, lse, prev=torch.zeros_like(c.mass), scale=scale)
     assert c.status() == 0
     check_mass(c, Q, lse, 1.0, torch.zeros_like(c.mass), scale)
+
+
+# ------------------------------------------------------------------ no tokens, one token
+@pytest.mark.parametrize("dtype,rows", KERNELS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_heads_that_hold_nothing_or_one_token(d, dtype, rows):
+    """Every head empty: zeros, lse -inf, weights and a smaller cache left as they were; then one
+    token each, in a graph that was captured over the empty cache."""
+    import torch
+    H, dt = 7, _dt(dtype)[0]
+    torch.manual_seed(rows)
+    c = poisoned(H, d, 64, 64, dtype, max_queries=rows)
+    to = poisoned(H, d, 64, 64, dtype)
+    Q = torch.randn(H, rows, d, device="cuda").to(dt)
+    O, lse = torch.full_like(Q, 5.0), torch.full((H, rows), 5.0, device="cuda")
+
+    def step():
+        c.attend(Q, O, lse)
+        c.accumulate(Q, lse)
+        c.evict(to, 1)
+
+    step()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for replay in (False, True):
+        if replay:
+            O.fill_(5.0)
+            g.replay()
+        assert bool((O == 0).all()) and bool(torch.isneginf(lse).all())
+        assert bool(c.mass.isnan().all()) and to.len.tolist() == [0] * H
+        for t in (to.K, to.V):
+            assert bool((t == 0x7F).all())
+    x = torch.randn(2, H, 1, d, device="cuda").to(dt)
+    c.append(x[0], x[1])
+    g.replay()
+    assert c.status() == 0 and to.len.tolist() == [1] * H
+    check_attend(c, Q, O, lse)
+    # one token takes all of a row's weight: 1, but for its score's two roundings
+    assert float((c.mass[:, 0] - rows).abs().max()) <= rows * 2.0 ** -10
+    assert torch.equal(to.K[:, 0], c.K[:, 0]) and torch.equal(to.mass[:, 0], c.mass[:, 0])

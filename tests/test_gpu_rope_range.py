@@ -38,3 +38,20 @@ def test_rope_stays_a_rotation(base, halves):
     tol = np.zeros_like(a)
     tol[..., i] = tol[..., j] = (np.abs(a[..., i]) + np.abs(a[..., j])) * (2.0 ** -21 + angle_off)
     assert np.all(np.abs(b - ref) <= tol)
+
+
+@pytest.mark.parametrize("inverse", [False, True])
+def test_rope_of_broadcast_rows(inverse):
+    """Rows of X that lie on one another (a stride of 0): heads that share a key, tokens that share
+    a row."""
+    import torch
+    import kv_cache_compression_post_b200 as kvb
+    torch.manual_seed(4)
+    H, n, d, pairs = 5, 9, 64, (12, 10, 10)
+    pos = torch.randint(-50, 3000, (n, 3), dtype=torch.int32, device="cuda")
+    for x in (torch.randn(1, n, d, device="cuda").expand(H, n, d), torch.randn(H, 1, d, device="cuda").expand(H, n, d),
+              torch.randn(1, 1, d, device="cuda").expand(H, n, d)):
+        y, z = torch.empty(H, n, d, device="cuda"), torch.empty(H, n, d, device="cuda")
+        kvb.rope(x, pos, y, pairs, inverse=inverse)
+        kvb.rope(x.contiguous(), pos, z, pairs, inverse=inverse)
+        assert torch.equal(y, z)
